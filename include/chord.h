@@ -414,6 +414,127 @@ chord_status chord_w4a16_moe_grouped(int mode, const uint16_t* a, int64_t M, int
                                      int flags, void* stream);
 
 /* ------------------------------------------------------------------------- */
+/* around the routed experts: scored router, 8-bit products, shared expert    */
+/* ------------------------------------------------------------------------- */
+/* Element types of the calls below. */
+#define CHORD_TYPE_F32 0
+#define CHORD_TYPE_BF16 1
+#define CHORD_TYPE_F16 2
+
+/* Scores of the router. */
+#define CHORD_SCORE_SOFTMAX 0
+#define CHORD_SCORE_SIGMOID 1
+
+/*
+ * Router with a choice of scores, a balance bias and expert groups.  Per token:
+ *   score     s_e = exp(x_e - max x) / sum exp(x - max x), or 1 / (1 + exp(-x_e));
+ *   choice    by c_e = s_e + bias_e (bias NULL: by the logits, whose order is
+ *             that of the scores).  With n_group > topk_group the E experts form
+ *             n_group groups of consecutive ids; a group's score is the sum of
+ *             the group_top (1 or 2) largest c_e of its experts (bias NULL: of
+ *             s_e, for softmax before the division by the sum), and only
+ *             experts of the topk_group best groups can be chosen.
+ *             topk_ids[t, 0..k): the k largest in descending order, ties (of
+ *             experts and of groups) to the lower id;
+ *   weight    topk_weights[t, j] = s of expert topk_ids[t, j] (without the bias),
+ *             divided by the sum of the k when renormalize != 0 (the ratios hold
+ *             even where every chosen score underflows), times scale.
+ * An expert whose logit is -inf or NaN is masked (as one whose bias is NaN):
+ * its score is 0, it ranks below every other, and a group's score leaves it out.  +inf counts
+ * as the largest finite float.  When fewer than k experts can be chosen, the
+ * remaining slots take the lowest ids not yet chosen, with weight 0, so that
+ * every id is valid and distinct.
+ * Arithmetic in fp32 whatever the logits' type.  The layer is reached with
+ * chord_moe_align of topk_ids.
+ *
+ *   logits   device [T, E] of `type`, rows ld elements apart (ld >= E)
+ *   bias     device float [E] or NULL
+ *   scale    finite
+ *   topk_ids device int32 [T, k], topk_weights device float [T, k] (outputs)
+ * Limits: E <= 1024, k <= 32, n_group <= 32 (CHORD_ERR_UNSUPPORTED_SHAPE);
+ *   E % n_group == 0, k <= topk_group * (E / n_group).  T = 0 is allowed.
+ */
+chord_status chord_moe_route(const void* logits, int type, int64_t T, int E, int64_t ld, int k,
+                             int scoring, const float* bias, int n_group, int topk_group,
+                             int group_top, int renormalize, float scale, int32_t* topk_ids,
+                             float* topk_weights, void* stream);
+
+/*
+ * Gradient of chord_moe_route's weights at its logits.  The choice (and with it
+ * the bias and the groups) is a constant.  d_weights, topk_ids and topk_weights
+ * are [T, k] (gradient of, and what chord_moe_route returned); scoring,
+ * renormalize and scale as there.  d_logits, device [T, E] of `type`, densely
+ * packed, is written entirely.  An id outside [0, E) gives no gradient.
+ */
+chord_status chord_moe_route_backward(const float* d_weights, const void* logits, int type,
+                                      int64_t T, int E, int64_t ld, int k, int scoring,
+                                      int renormalize, float scale, const int32_t* topk_ids,
+                                      const float* topk_weights, void* d_logits, void* stream);
+
+/*
+ * Rows quantised to 8-bit integers.  Per row with largest magnitude m:
+ *   scale = m / 127,  q = rint(x * (127 * (1 / m)))     (fp32 operations in this
+ *   order, ties to even).
+ * A row with m < 2^-100 gets scale 0 and codes 0; a row that holds an inf or a
+ * NaN gets scale NaN and codes 0, so that its products are NaN.
+ * chord_int8_silu_mul_quantize does so with x = silu(gate) * up, gate =
+ * gate_up[t, 0..I), up = gate_up[t, I..2I).
+ * Serves tokens (a scale per token) and weights [N, K] (a scale per channel).
+ *   x, gate_up  device [T, K], [T, 2I] of `type`, rows ld_x elements apart; rows
+ *               that start on 16-byte boundaries are read fastest
+ *   q           device int8 [T, K], 16-byte aligned, rows ld_q bytes apart,
+ *               ld_q % 16 == 0 (bytes past K are not written)
+ *   scale       device float [T]
+ * Limits: 1 <= K <= 131071 (CHORD_ERR_UNSUPPORTED_SHAPE).  T = 0 is allowed.
+ */
+chord_status chord_int8_quantize(const void* x, int type, int64_t T, int K, int64_t ld_x, int8_t* q,
+                                 int64_t ld_q, float* scale, void* stream);
+chord_status chord_int8_silu_mul_quantize(const void* gate_up, int type, int64_t T, int I,
+                                          int64_t ld_x, int8_t* q, int64_t ld_q, float* scale,
+                                          void* stream);
+
+/*
+ * Product of 8-bit integers with a scale per token and per channel:
+ *   out[t, n] = (sum_k a[t, k] * w[n, k]) * a_scale[t] * w_scale[n] (+ residual[t, n])
+ * The sum is exact (32-bit integer), whatever the sizes and the schedule, so
+ * the result is bit-reproducible; scales, sum with the residual and one
+ * rounding to `type` in fp32.
+ *   a         device int8 [T, K], 16-byte aligned, rows ld_a bytes apart
+ *   w         device int8 [N, K], 16-byte aligned, rows ld_w bytes apart
+ *             (ld_a, ld_w >= K and % 16 == 0; bytes past K are ignored)
+ *   a_scale   device float [T];  w_scale device float [N]
+ *   residual  device [T, N] of `type`, rows ld_r elements apart, or NULL; may be
+ *             `out` itself (same rows and ld)
+ *   out       device [T, N] of `type`, rows ld_out elements apart
+ *   workspace device, >= 256 bytes, 256-aligned (the device error word)
+ *   flags     0 or CHORD_FLAG_VALIDATE
+ * Limits: 1 <= K <= 131071, N >= 1.  T = 0 is allowed.
+ *
+ * chord_int8_linear: x [T, K] of `type` quantised per token, then the product.
+ * chord_int8_mlp: a gated MLP (a shared expert) in 8-bit integers:
+ *   g, u = the rows 0..I-1, I..2I-1 of w13 [2I, H] times quantised x [T, H];
+ *   out = w2 [H, I] times quantised silu(g) * u, plus the residual (the routed
+ *   experts' output); g and u stay in fp32.
+ * Their workspace: chord_int8_workspace_size(T, K, 0) and (T, H, I) bytes (0 for
+ * bad arguments).
+ */
+size_t chord_int8_workspace_size(int64_t T, int K, int I);
+chord_status chord_int8_matmul(const int8_t* a, int64_t ld_a, const float* a_scale, const int8_t* w,
+                               int64_t ld_w, const float* w_scale, int64_t T, int N, int K,
+                               const void* residual, int64_t ld_r, void* out, int type,
+                               int64_t ld_out, void* workspace, size_t workspace_bytes, int flags,
+                               void* stream);
+chord_status chord_int8_linear(const void* x, int type, int64_t ld_x, const int8_t* w, int64_t ld_w,
+                               const float* w_scale, int64_t T, int N, int K, const void* residual,
+                               int64_t ld_r, void* out, int64_t ld_out, void* workspace,
+                               size_t workspace_bytes, int flags, void* stream);
+chord_status chord_int8_mlp(const void* x, int type, int64_t ld_x, const int8_t* w13, int64_t ld_w13,
+                            const float* w13_scale, const int8_t* w2, int64_t ld_w2,
+                            const float* w2_scale, int64_t T, int H, int I, const void* residual,
+                            int64_t ld_r, void* out, int64_t ld_out, void* workspace,
+                            size_t workspace_bytes, int flags, void* stream);
+
+/* ------------------------------------------------------------------------- */
 /* device error word                                                          */
 /* ------------------------------------------------------------------------- */
 /* Synchronises `stream`, copies the error word of `workspace` (of a layer or

@@ -28,6 +28,18 @@ from .ops import (  # noqa: F401
     w4a16_moe_grouped,
     w4a16_moe_indexed,
 )
+from .block import (  # noqa: F401
+    int8_linear,
+    int8_matmul,
+    int8_mlp,
+    int8_quantize,
+    int8_rows,
+    int8_silu_mul_quantize,
+    int8_workspace_size,
+    moe_block,
+    moe_route,
+    moe_route_backward,
+)
 from . import synth  # noqa: F401
 
 __all__ = [
@@ -36,4 +48,6 @@ __all__ = [
     "prepack", "prepack_size", "prepack_weights", "select_block_m",
     "stage_timing_enable", "stage_timing_read", "w4a16_moe", "w4a16_moe_grouped",
     "w4a16_moe_indexed", "synth",
+    "moe_route", "moe_route_backward", "int8_quantize", "int8_silu_mul_quantize", "int8_rows",
+    "int8_matmul", "int8_workspace_size", "int8_linear", "int8_mlp", "moe_block",
 ]

@@ -41,9 +41,15 @@ DEVERR_ROUTING = 2
 DEVERR_CAPACITY = 4
 DEVERR_SCALE_RANGE = 8
 DEVERR_PACKED = 16
+TYPE_F32 = 0
+TYPE_BF16 = 1
+TYPE_F16 = 2
+SCORE_SOFTMAX = 0
+SCORE_SIGMOID = 1
 
 # every symbol include/chord.h declares, with (restype, argtypes)
 _i64, _int, _sz, _vp, _cp = ctypes.c_int64, ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_char_p
+_f32 = ctypes.c_float
 SIGNATURES = {
     "chord_status_string": (_cp, [_int]),
     "chord_version": (_int, []),
@@ -69,6 +75,19 @@ SIGNATURES = {
     "chord_w4a16_moe_grouped": (_int, [_int, _vp, _i64, _int, _int, _int, _vp, _vp, _i64, _int,
                                        _vp, _vp, _vp, _vp, _vp, _vp, _i64, _int, _vp, _sz, _vp,
                                        _vp, _vp, _int, _vp]),
+    "chord_moe_route": (_int, [_vp, _int, _i64, _int, _i64, _int, _int, _vp, _int, _int, _int, _int,
+                               _f32, _vp, _vp, _vp]),
+    "chord_moe_route_backward": (_int, [_vp, _vp, _int, _i64, _int, _i64, _int, _int, _int, _f32,
+                                        _vp, _vp, _vp, _vp]),
+    "chord_int8_quantize": (_int, [_vp, _int, _i64, _int, _i64, _vp, _i64, _vp, _vp]),
+    "chord_int8_silu_mul_quantize": (_int, [_vp, _int, _i64, _int, _i64, _vp, _i64, _vp, _vp]),
+    "chord_int8_workspace_size": (_sz, [_i64, _int, _int]),
+    "chord_int8_matmul": (_int, [_vp, _i64, _vp, _vp, _i64, _vp, _i64, _int, _int, _vp, _i64, _vp,
+                                 _int, _i64, _vp, _sz, _int, _vp]),
+    "chord_int8_linear": (_int, [_vp, _int, _i64, _vp, _i64, _vp, _i64, _int, _int, _vp, _i64, _vp,
+                                 _i64, _vp, _sz, _int, _vp]),
+    "chord_int8_mlp": (_int, [_vp, _int, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _i64, _int, _int,
+                              _vp, _i64, _vp, _i64, _vp, _sz, _int, _vp]),
     "chord_get_device_error": (_int, [_vp, ctypes.POINTER(ctypes.c_int), _int, _vp]),
     "chord_stage_timing_enable": (_int, [_int]),
     "chord_stage_timing_read": (_int, [ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_int)]),

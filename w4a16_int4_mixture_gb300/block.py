@@ -1,0 +1,296 @@
+"""PyTorch-facing calls of the operators around the routed experts.
+
+The scored router and its gradient, products in 8-bit integers with a scale per
+token and per channel, the shared expert built of them, and the whole mixture
+block.  Like ops.py, thin wrappers over the C ABI (include/chord.h).
+
+Layouts (rows may lie further apart than they are long; elements of a row are
+contiguous):
+  logits       float32 / bfloat16 / float16 [T, E]
+  x, residual  float32 / bfloat16 / float16 [T, H]
+  codes        int8 [T, K] or [N, K], rows on 16-byte boundaries; scales float32 [T] or [N]
+"""
+
+from __future__ import annotations
+
+from typing import Optional
+
+import torch
+
+from . import _binding as B
+from . import ops
+
+_TYPES = {torch.float32: B.TYPE_F32, torch.bfloat16: B.TYPE_BF16, torch.float16: B.TYPE_F16}
+_SCORES = {"softmax": B.SCORE_SOFTMAX, "sigmoid": B.SCORE_SIGMOID}
+_F32 = (torch.float32,)
+_I32 = (torch.int32,)
+_I8 = (torch.int8,)
+
+
+def _rows(t, name: str, dtypes, dev=None, shape=None) -> int:
+    """Checks a 2-d tensor of rows with contiguous elements; -> the distance of its rows."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype} not in {tuple(dtypes)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dev is not None and t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dims")
+    n, m = t.shape
+    if shape is not None and (n, m) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {[n, m]}")
+    ld, one = t.stride()
+    if m > 1 and one != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    if n <= 1:
+        return max(m, 1)
+    if ld < m:
+        raise ValueError(f"{name}: rows overlap (stride {ld} < {m})")
+    return ld
+
+
+def _codes(t, name: str, dev=None, shape=None) -> int:
+    ld = _rows(t, name, _I8, dev, shape)
+    if t.shape[0] <= 1:
+        ld = (t.shape[1] + 15) // 16 * 16
+    if ld % 16 or (t.data_ptr() % 16 and t.numel()):
+        raise ValueError(f"{name}: rows must start on 16-byte boundaries "
+                         "(int8_quantize returns such rows, int8_rows copies codes to them)")
+    return ld
+
+
+def _vec(t, name: str, dev, n: int):
+    ops._req(t, name, _F32, dev, 1)
+    if t.numel() != n:
+        raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
+
+
+def _residual(t, dev, dtype, shape) -> int:
+    return 0 if t is None else _rows(t, "residual", (dtype,), dev, shape)
+
+
+def _workspace(ws, dev, need: int):
+    # (allocated on the current stream, so that calls on several streams do not share it)
+    return torch.empty(need, dtype=torch.uint8, device=dev) if ws is None else ws
+
+
+def moe_route(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = None,
+              scoring: str = "softmax", n_group: int = 1, topk_group: int = 1, group_top: int = 2,
+              renormalize: bool = True, scale: float = 1.0, out=None):
+    """Router logits [T, E] -> (topk_ids int32 [T, k], topk_weights float32 [T, k]).
+
+    Scores are the softmax or the sigmoids of the logits.  The k experts are chosen by score +
+    bias (float32 [E]) among the experts of the topk_group groups (of n_group) with the largest
+    sums of their group_top best; the weights are the scores without the bias, divided by their
+    sum when renormalize, times scale.  Experts with a logit of -inf or NaN are masked.  out:
+    (topk_ids, topk_weights) to write."""
+    ld = _rows(logits, "logits", _TYPES)
+    if scoring not in _SCORES:
+        raise ValueError(f"unknown scoring {scoring!r}")
+    dev = logits.device
+    T, E = logits.shape
+    if bias is not None:
+        _vec(bias, "bias", dev, E)
+    if out is None:
+        ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+        weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+    else:
+        ids, weights = out
+        _pairs(ids, weights, dev, T, k)
+    st = ops.lib().chord_moe_route(ops._p(logits), _TYPES[logits.dtype], T, E, ld, k,
+                                   _SCORES[scoring], ops._p(bias), n_group, topk_group, group_top,
+                                   1 if renormalize else 0, scale, ops._p(ids), ops._p(weights),
+                                   ops._stream(dev))
+    B.check(st, "chord_moe_route")
+    return ids, weights
+
+
+def _pairs(ids, weights, dev, T, k):
+    ops._req(ids, "topk_ids", _I32, dev, 2)
+    ops._req(weights, "topk_weights", _F32, dev, 2)
+    if tuple(ids.shape) != (T, k) or tuple(weights.shape) != (T, k):
+        raise ValueError(f"topk_ids and topk_weights must be [{T}, {k}]")
+
+
+def moe_route_backward(d_weights: torch.Tensor, logits: torch.Tensor, topk_ids: torch.Tensor,
+                       topk_weights: torch.Tensor, scoring: str = "softmax",
+                       renormalize: bool = True, scale: float = 1.0, out=None) -> torch.Tensor:
+    """Gradient at the logits (their type, [T, E]) of moe_route's weights, given d_weights
+    float32 [T, k] and what moe_route was given and returned.  The choice is a constant."""
+    ld = _rows(logits, "logits", _TYPES)
+    if scoring not in _SCORES:
+        raise ValueError(f"unknown scoring {scoring!r}")
+    dev = logits.device
+    T, E = logits.shape
+    ops._req(d_weights, "d_weights", _F32, dev, 2)
+    if d_weights.shape[0] != T:
+        raise ValueError("d_weights and logits disagree on T")
+    k = d_weights.shape[1]
+    _pairs(topk_ids, topk_weights, dev, T, k)
+    if out is None:
+        out = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    else:
+        ops._req(out, "out", (logits.dtype,), dev, 2)
+        if tuple(out.shape) != (T, E):
+            raise ValueError(f"out must be [{T}, {E}]")
+    st = ops.lib().chord_moe_route_backward(ops._p(d_weights), ops._p(logits), _TYPES[logits.dtype],
+                                            T, E, ld, k, _SCORES[scoring], 1 if renormalize else 0,
+                                            scale, ops._p(topk_ids), ops._p(topk_weights),
+                                            ops._p(out), ops._stream(dev))
+    B.check(st, "chord_moe_route_backward")
+    return out
+
+
+def int8_rows(codes: torch.Tensor) -> torch.Tensor:
+    """Codes int8 [N, K] copied to rows that start on 16-byte boundaries."""
+    N, K = codes.shape
+    q = torch.empty((N, (K + 15) // 16 * 16), dtype=torch.int8, device=codes.device)[:, :K]
+    q.copy_(codes)
+    return q
+
+
+def _quantize(x, K: int, ld: int, out, fn: str):
+    dev = x.device
+    T = x.shape[0]
+    if out is None:
+        q = torch.empty((T, (K + 15) // 16 * 16), dtype=torch.int8, device=dev)[:, :K]
+        scale = torch.empty(T, dtype=torch.float32, device=dev)
+    else:
+        q, scale = out
+        _vec(scale, "scale", dev, T)
+    ld_q = _codes(q, "codes", dev, (T, K))
+    st = getattr(ops.lib(), fn)(ops._p(x), _TYPES[x.dtype], T, K, ld, ops._p(q), ld_q,
+                                ops._p(scale), ops._stream(dev))
+    B.check(st, fn)
+    return q, scale
+
+
+def int8_quantize(x: torch.Tensor, out=None):
+    """Rows of x [T, K] -> (codes int8 [T, K], scales float32 [T]): scale = max|x| / 127, codes =
+    rint(x * (127 * (1 / max|x|))).  For tokens and for weights [N, K].  A row holding an inf or NaN
+    gets the scale NaN.  The codes' rows start on 16-byte boundaries."""
+    return _quantize(x, x.shape[-1], _rows(x, "x", _TYPES), out, "chord_int8_quantize")
+
+
+def int8_silu_mul_quantize(gate_up: torch.Tensor, out=None):
+    """gate_up [T, 2I] -> int8_quantize(silu(gate_up[:, :I]) * gate_up[:, I:]), in one pass."""
+    ld = _rows(gate_up, "gate_up", _TYPES)
+    if gate_up.shape[1] % 2:
+        raise ValueError("gate_up must have an even number of columns")
+    return _quantize(gate_up, gate_up.shape[1] // 2, ld, out, "chord_int8_silu_mul_quantize")
+
+
+def _output(out, dev, dtype, shape):
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dev)
+        return out, shape[1]
+    return out, _rows(out, "out", (dtype,), dev, shape)
+
+
+def int8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+                residual: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+                out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                flags: int = 0) -> torch.Tensor:
+    """out [T, N] = (a [T, K] int8 @ w [N, K]^T int8) * a_scale[:, None] * w_scale + residual,
+    the product exact in 32-bit integers, one rounding to out_dtype (out's type when given)."""
+    ld_a = _codes(a, "a")
+    dev = a.device
+    T, K = a.shape
+    if out is not None:
+        out_dtype = out.dtype
+    if out_dtype not in _TYPES:
+        raise TypeError(f"out_dtype {out_dtype} not in {tuple(_TYPES)}")
+    ld_w = _codes(w, "w", dev)
+    N = w.shape[0]
+    if w.shape[1] != K:
+        raise ValueError(f"a and w disagree on K ({K}, {w.shape[1]})")
+    _vec(a_scale, "a_scale", dev, T)
+    _vec(w_scale, "w_scale", dev, N)
+    ld_r = _residual(residual, dev, out_dtype, (T, N))
+    out, ld_out = _output(out, dev, out_dtype, (T, N))
+    ws = _workspace(workspace, dev, 256)
+    st = ops.lib().chord_int8_matmul(ops._p(a), ld_a, ops._p(a_scale), ops._p(w), ld_w,
+                                     ops._p(w_scale), T, N, K, ops._p(residual), ld_r, ops._p(out),
+                                     _TYPES[out_dtype], ld_out, ops._p(ws), ws.numel(), flags,
+                                     ops._stream(dev))
+    B.check(st, "chord_int8_matmul")
+    return out
+
+
+def int8_workspace_size(T: int, K: int, I: int = 0) -> int:
+    """Workspace bytes of int8_linear (T, K) and of int8_mlp (T, H, I)."""
+    return int(ops.lib().chord_int8_workspace_size(T, K, I))
+
+
+def int8_linear(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+                residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                workspace: Optional[torch.Tensor] = None, flags: int = 0) -> torch.Tensor:
+    """x [T, K] quantised per token, times w [N, K] int8 (w_scale [N]), plus residual; x's type."""
+    ld_x = _rows(x, "x", _TYPES)
+    dev = x.device
+    T, K = x.shape
+    ld_w = _codes(w, "w", dev)
+    N = w.shape[0]
+    if w.shape[1] != K:
+        raise ValueError(f"x and w disagree on K ({K}, {w.shape[1]})")
+    _vec(w_scale, "w_scale", dev, N)
+    ld_r = _residual(residual, dev, x.dtype, (T, N))
+    out, ld_out = _output(out, dev, x.dtype, (T, N))
+    ws = _workspace(workspace, dev, int8_workspace_size(T, K))
+    st = ops.lib().chord_int8_linear(ops._p(x), _TYPES[x.dtype], ld_x, ops._p(w), ld_w,
+                                     ops._p(w_scale), T, N, K, ops._p(residual), ld_r, ops._p(out),
+                                     ld_out, ops._p(ws), ws.numel(), flags, ops._stream(dev))
+    B.check(st, "chord_int8_linear")
+    return out
+
+
+def int8_mlp(x: torch.Tensor, w13: torch.Tensor, w13_scale: torch.Tensor, w2: torch.Tensor,
+             w2_scale: torch.Tensor, residual: Optional[torch.Tensor] = None,
+             out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+             flags: int = 0) -> torch.Tensor:
+    """Gated MLP in 8-bit integers (a shared expert): x [T, H], w13 int8 [2I, H] (rows 0..I-1
+    gate, I..2I-1 up), w2 int8 [H, I]; out = w2 (silu(g) * u) + residual, in x's type.  x and
+    silu(g) * u are quantised per token; pass the routed experts' output as the residual (out may
+    be the same tensor)."""
+    ld_x = _rows(x, "x", _TYPES)
+    dev = x.device
+    T, H = x.shape
+    ld13 = _codes(w13, "w13", dev)
+    I = w13.shape[0] // 2
+    if tuple(w13.shape) != (2 * I, H) or I < 1:
+        raise ValueError("w13 must be [2I, H]")
+    ld2 = _codes(w2, "w2", dev, (H, I))
+    _vec(w13_scale, "w13_scale", dev, 2 * I)
+    _vec(w2_scale, "w2_scale", dev, H)
+    ld_r = _residual(residual, dev, x.dtype, (T, H))
+    out, ld_out = _output(out, dev, x.dtype, (T, H))
+    ws = _workspace(workspace, dev, int8_workspace_size(T, H, I))
+    st = ops.lib().chord_int8_mlp(ops._p(x), _TYPES[x.dtype], ld_x, ops._p(w13), ld13,
+                                  ops._p(w13_scale), ops._p(w2), ld2, ops._p(w2_scale), T, H, I,
+                                  ops._p(residual), ld_r, ops._p(out), ld_out, ops._p(ws),
+                                  ws.numel(), flags, ops._stream(dev))
+    B.check(st, "chord_int8_mlp")
+    return out
+
+
+def moe_block(x: torch.Tensor, logits: torch.Tensor, k: int, experts, shared=None,
+              bias: Optional[torch.Tensor] = None, scoring: str = "sigmoid", n_group: int = 1,
+              topk_group: int = 1, group_top: int = 2, renormalize: bool = True, scale: float = 1.0,
+              expert_map: Optional[torch.Tensor] = None, flags: int = 0) -> torch.Tensor:
+    """A mixture block: moe_route of the router's logits [T, E], the routed experts (w4a16_moe)
+    and, added to their output, the shared expert (int8_mlp).
+
+    x bf16 [T, H]; experts: PackedWeights or (w13_q, w13_s, w2_q, w2_s); shared: None or (w13,
+    w13_scale, w2, w2_scale) in 8-bit integers.  Returns bf16 [T, H]."""
+    ids, weights = moe_route(logits, k, bias=bias, scoring=scoring, n_group=n_group,
+                             topk_group=topk_group, group_top=group_top, renormalize=renormalize,
+                             scale=scale)
+    w = (experts, None, None, None) if isinstance(experts, ops.PackedWeights) else tuple(experts)
+    y = ops.w4a16_moe(x, ids, weights, *w, E_global=logits.shape[1], expert_map=expert_map,
+                      flags=flags)
+    if shared is None:
+        return y
+    return int8_mlp(x, *shared, residual=y, out=y, flags=flags & B.FLAG_VALIDATE)

@@ -1,0 +1,284 @@
+// block_api.cu -- the C ABI of the operators around the routed experts
+// (include/chord.h): argument checks, workspace layout and the launches.
+#include <cmath>
+
+#include "block_kernels.h"
+
+using namespace chord;
+
+namespace {
+
+constexpr size_t kAlign = 256;
+constexpr size_t kHeader = 256;  // the device error word
+constexpr int kMaxK = 131071;    // |sum of K products of 8-bit integers| < 2^31
+
+size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
+int64_t pad16(int64_t k) { return (k + 15) / 16 * 16; }
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool type_ok(int type) { return type == CHORD_TYPE_F32 || type == CHORD_TYPE_BF16 || type == CHORD_TYPE_F16; }
+bool scoring_ok(int s) { return s == CHORD_SCORE_SOFTMAX || s == CHORD_SCORE_SIGMOID; }
+// rows of n elements, ld apart (one row: any ld)
+bool ld_ok(int64_t rows, int64_t n, int64_t ld) { return ld >= n || (rows <= 1 && ld >= 0); }
+
+chord_status check_ws(void* ws, size_t bytes, size_t need)
+{
+    if (!ws || bytes < need || reinterpret_cast<uintptr_t>(ws) % kAlign != 0)
+        return CHORD_ERR_WORKSPACE;
+    return CHORD_OK;
+}
+
+// Sizes of a product of T tokens: every index below fits 63 bits and every
+// launch its grid.
+bool sizes_ok(int64_t T, int64_t N, int64_t K)
+{
+    return T < (int64_t(1) << 31) && N >= 1 && N < (int64_t(1) << 30) && K >= 1 && K <= kMaxK;
+}
+
+chord_status finish(int flags, void* ws, cudaStream_t s)
+{
+    if (!(flags & CHORD_FLAG_VALIDATE))
+        return CHORD_OK;
+    return chord_get_device_error(ws, nullptr, 0, s);
+}
+
+struct Scratch {  // of chord_int8_linear and chord_int8_mlp
+    size_t codes, scales, mid, codes2, scales2, total;
+};
+Scratch scratch(int64_t T, int K, int I)
+{
+    Scratch p{};
+    size_t at = kHeader;
+    auto take = [&](size_t bytes) {
+        const size_t r = at;
+        at += align_up(bytes);
+        return r;
+    };
+    p.codes = take(static_cast<size_t>(T) * pad16(K));
+    p.scales = take(static_cast<size_t>(T) * 4);
+    if (I > 0) {
+        p.mid = take(static_cast<size_t>(T) * 2 * I * 4);
+        p.codes2 = take(static_cast<size_t>(T) * pad16(I));
+        p.scales2 = take(static_cast<size_t>(T) * 4);
+    }
+    p.total = at;
+    return p;
+}
+
+cudaError_t product(const Int8Args& a, const DeviceInfo& dev, cudaStream_t s)
+{
+    return launch_int8_rows(a, dev.sms, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+chord_status chord_moe_route(const void* logits, int type, int64_t T, int E, int64_t ld, int k,
+                             int scoring, const float* bias, int n_group, int topk_group,
+                             int group_top, int renormalize, float scale, int32_t* topk_ids,
+                             float* topk_weights, void* stream)
+{
+    if (!type_ok(type) || !scoring_ok(scoring) || T < 0 || E < 1 || k < 1 || !ld_ok(T, E, ld) ||
+        n_group < 1 || topk_group < 1 || topk_group > n_group || group_top < 1 || group_top > 2 ||
+        !std::isfinite(scale))
+        return CHORD_ERR_INVALID_ARG;
+    if (E > 1024 || k > 32 || n_group > 32 || T >= (int64_t(1) << 31))
+        return CHORD_ERR_UNSUPPORTED_SHAPE;
+    if (E % n_group != 0 || k > topk_group * (E / n_group))
+        return CHORD_ERR_INVALID_ARG;
+    if (T == 0)
+        return CHORD_OK;
+    if (!logits || !topk_ids || !topk_weights)
+        return CHORD_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    chord_status st = device_info(&dev);
+    if (st != CHORD_OK)
+        return st;
+    // (all groups kept: the groups do not steer the choice)
+    if (topk_group == n_group)
+        n_group = topk_group = 1;
+    const MoeRouteArgs a{logits,  type,       T,         ld,              E,     k,        scoring,     bias,
+                         n_group, topk_group, group_top, renormalize ? 1 : 0, scale, topk_ids, topk_weights};
+    PdlScope pdl(T <= kPdlMaxRows);
+    return from_cuda(launch_moe_route(a, dev.sms, static_cast<cudaStream_t>(stream)));
+}
+
+chord_status chord_moe_route_backward(const float* d_weights, const void* logits, int type,
+                                      int64_t T, int E, int64_t ld, int k, int scoring,
+                                      int renormalize, float scale, const int32_t* topk_ids,
+                                      const float* topk_weights, void* d_logits, void* stream)
+{
+    if (!type_ok(type) || !scoring_ok(scoring) || T < 0 || E < 1 || k < 1 || k > E ||
+        !ld_ok(T, E, ld) || !std::isfinite(scale))
+        return CHORD_ERR_INVALID_ARG;
+    if (E > 1024 || k > 32 || T >= (int64_t(1) << 31))
+        return CHORD_ERR_UNSUPPORTED_SHAPE;
+    if (T == 0)
+        return CHORD_OK;
+    if (!d_weights || !logits || !topk_ids || !topk_weights || !d_logits)
+        return CHORD_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    chord_status st = device_info(&dev);
+    if (st != CHORD_OK)
+        return st;
+    const MoeRouteBwdArgs a{d_weights, logits, type,  T,        ld,           E,       k,
+                            scoring,   renormalize ? 1 : 0, scale, topk_ids, topk_weights, d_logits};
+    PdlScope pdl(T <= kPdlMaxRows);
+    return from_cuda(launch_moe_route_backward(a, dev.sms, static_cast<cudaStream_t>(stream)));
+}
+
+static chord_status quantize(const void* x, int type, int64_t T, int K, int64_t ld_x, int8_t* q,
+                             int64_t ld_q, float* scale, int silu_mul, void* stream)
+{
+    if (!type_ok(type) || T < 0 || K < 1 || !ld_ok(T, silu_mul ? 2 * int64_t(K) : K, ld_x) ||
+        !ld_ok(T, K, ld_q) || ld_q % 16 != 0)
+        return CHORD_ERR_INVALID_ARG;
+    if (!sizes_ok(T, 1, K))
+        return CHORD_ERR_UNSUPPORTED_SHAPE;
+    if (T == 0)
+        return CHORD_OK;
+    if (!x || !q || !scale || !aligned16(q))
+        return CHORD_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    chord_status st = device_info(&dev);
+    if (st != CHORD_OK)
+        return st;
+    const QuantArgs a{x, type, T, K, ld_x, q, ld_q, scale, silu_mul, nullptr};
+    PdlScope pdl(T <= kPdlMaxRows);
+    return from_cuda(launch_int8_quantize(a, dev.sms, static_cast<cudaStream_t>(stream)));
+}
+
+chord_status chord_int8_quantize(const void* x, int type, int64_t T, int K, int64_t ld_x, int8_t* q,
+                                 int64_t ld_q, float* scale, void* stream)
+{
+    return quantize(x, type, T, K, ld_x, q, ld_q, scale, 0, stream);
+}
+
+chord_status chord_int8_silu_mul_quantize(const void* gate_up, int type, int64_t T, int I,
+                                          int64_t ld_x, int8_t* q, int64_t ld_q, float* scale,
+                                          void* stream)
+{
+    return quantize(gate_up, type, T, I, ld_x, q, ld_q, scale, 1, stream);
+}
+
+size_t chord_int8_workspace_size(int64_t T, int K, int I)
+{
+    if (T < 0 || !sizes_ok(T, 1, K) || I < 0 || I > kMaxK)
+        return 0;
+    return scratch(T, K, I).total;
+}
+
+chord_status chord_int8_matmul(const int8_t* a, int64_t ld_a, const float* a_scale, const int8_t* w,
+                               int64_t ld_w, const float* w_scale, int64_t T, int N, int K,
+                               const void* residual, int64_t ld_r, void* out, int type,
+                               int64_t ld_out, void* workspace, size_t workspace_bytes, int flags,
+                               void* stream)
+{
+    if (!type_ok(type) || T < 0 || N < 1 || K < 1 || (flags & ~CHORD_FLAG_VALIDATE) ||
+        !ld_ok(T, K, ld_a) || !ld_ok(N, K, ld_w) || !ld_ok(T, N, ld_out) ||
+        (residual && !ld_ok(T, N, ld_r)) || ld_a % 16 != 0 || ld_w % 16 != 0)
+        return CHORD_ERR_INVALID_ARG;
+    if (!sizes_ok(T, N, K))
+        return CHORD_ERR_UNSUPPORTED_SHAPE;
+    if (T == 0)
+        return CHORD_OK;
+    if (!a || !a_scale || !w || !w_scale || !out || !aligned16(a) || !aligned16(w))
+        return CHORD_ERR_INVALID_ARG;
+    chord_status st = check_ws(workspace, workspace_bytes, kHeader);
+    if (st != CHORD_OK)
+        return st;
+    DeviceInfo dev;
+    if ((st = device_info(&dev)) != CHORD_OK)
+        return st;
+    const Int8Args g{a,        w,    ld_a, ld_w,   a_scale, w_scale, T, N, K,
+                     residual, ld_r, out,  ld_out, type,    static_cast<int*>(workspace), 1};
+    PdlScope pdl(T <= kPdlMaxRows);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (product(g, dev, s) != cudaSuccess)
+        return CHORD_ERR_CUDA;
+    return finish(flags, workspace, s);
+}
+
+chord_status chord_int8_linear(const void* x, int type, int64_t ld_x, const int8_t* w, int64_t ld_w,
+                               const float* w_scale, int64_t T, int N, int K, const void* residual,
+                               int64_t ld_r, void* out, int64_t ld_out, void* workspace,
+                               size_t workspace_bytes, int flags, void* stream)
+{
+    if (!type_ok(type) || T < 0 || N < 1 || K < 1 || (flags & ~CHORD_FLAG_VALIDATE) ||
+        !ld_ok(T, K, ld_x) || !ld_ok(N, K, ld_w) || !ld_ok(T, N, ld_out) ||
+        (residual && !ld_ok(T, N, ld_r)) || ld_w % 16 != 0)
+        return CHORD_ERR_INVALID_ARG;
+    if (!sizes_ok(T, N, K))
+        return CHORD_ERR_UNSUPPORTED_SHAPE;
+    if (T == 0)
+        return CHORD_OK;
+    if (!x || !w || !w_scale || !out || !aligned16(w))
+        return CHORD_ERR_INVALID_ARG;
+    const Scratch p = scratch(T, K, 0);
+    chord_status st = check_ws(workspace, workspace_bytes, p.total);
+    if (st != CHORD_OK)
+        return st;
+    DeviceInfo dev;
+    if ((st = device_info(&dev)) != CHORD_OK)
+        return st;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    int* err = static_cast<int*>(workspace);
+    int8_t* q = reinterpret_cast<int8_t*>(ws + p.codes);
+    float* qs = reinterpret_cast<float*>(ws + p.scales);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    PdlScope pdl(T <= kPdlMaxRows);
+    const QuantArgs qa{x, type, T, K, ld_x, q, pad16(K), qs, 0, err};
+    const Int8Args g{q,        w,    pad16(K), ld_w,   qs,   w_scale, T, N, K,
+                     residual, ld_r, out,      ld_out, type, err,     0};
+    if (launch_int8_quantize(qa, dev.sms, s) != cudaSuccess || product(g, dev, s) != cudaSuccess)
+        return CHORD_ERR_CUDA;
+    return finish(flags, workspace, s);
+}
+
+chord_status chord_int8_mlp(const void* x, int type, int64_t ld_x, const int8_t* w13, int64_t ld_w13,
+                            const float* w13_scale, const int8_t* w2, int64_t ld_w2,
+                            const float* w2_scale, int64_t T, int H, int I, const void* residual,
+                            int64_t ld_r, void* out, int64_t ld_out, void* workspace,
+                            size_t workspace_bytes, int flags, void* stream)
+{
+    if (!type_ok(type) || T < 0 || H < 1 || I < 1 || (flags & ~CHORD_FLAG_VALIDATE) ||
+        !ld_ok(T, H, ld_x) || !ld_ok(2, H, ld_w13) || !ld_ok(H, I, ld_w2) || !ld_ok(T, H, ld_out) ||
+        (residual && !ld_ok(T, H, ld_r)) || ld_w13 % 16 != 0 || ld_w2 % 16 != 0)
+        return CHORD_ERR_INVALID_ARG;
+    if (!sizes_ok(T, 2 * int64_t(I), H) || !sizes_ok(T, H, I))
+        return CHORD_ERR_UNSUPPORTED_SHAPE;
+    if (T == 0)
+        return CHORD_OK;
+    if (!x || !w13 || !w13_scale || !w2 || !w2_scale || !out || !aligned16(w13) || !aligned16(w2))
+        return CHORD_ERR_INVALID_ARG;
+    const Scratch p = scratch(T, H, I);
+    chord_status st = check_ws(workspace, workspace_bytes, p.total);
+    if (st != CHORD_OK)
+        return st;
+    DeviceInfo dev;
+    if ((st = device_info(&dev)) != CHORD_OK)
+        return st;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    int* err = static_cast<int*>(workspace);
+    int8_t* q = reinterpret_cast<int8_t*>(ws + p.codes);
+    float* qs = reinterpret_cast<float*>(ws + p.scales);
+    float* mid = reinterpret_cast<float*>(ws + p.mid);
+    int8_t* q2 = reinterpret_cast<int8_t*>(ws + p.codes2);
+    float* qs2 = reinterpret_cast<float*>(ws + p.scales2);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    PdlScope pdl(T <= kPdlMaxRows);
+    // gate and up stay in fp32 between the products: rounding them to 16 bits
+    // would move codes of the second quantisation
+    const QuantArgs qa{x, type, T, H, ld_x, q, pad16(H), qs, 0, err};
+    const Int8Args g1{q,       w13, pad16(H), ld_w13,         qs,             w13_scale, T, 2 * I, H,
+                      nullptr, 0,   mid,      2 * int64_t(I), CHORD_TYPE_F32, err,       0};
+    const QuantArgs ha{mid, CHORD_TYPE_F32, T, I, 2 * int64_t(I), q2, pad16(I), qs2, 1, nullptr};
+    const Int8Args g2{q2,       w2,   pad16(I), ld_w2,  qs2,  w2_scale, T, H, I,
+                      residual, ld_r, out,      ld_out, type, err,      0};
+    if (launch_int8_quantize(qa, dev.sms, s) != cudaSuccess || product(g1, dev, s) != cudaSuccess ||
+        launch_int8_quantize(ha, dev.sms, s) != cudaSuccess || product(g2, dev, s) != cudaSuccess)
+        return CHORD_ERR_CUDA;
+    return finish(flags, workspace, s);
+}
+
+}  // extern "C"

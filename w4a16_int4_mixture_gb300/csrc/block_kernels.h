@@ -1,0 +1,126 @@
+// block_kernels.h -- launch interfaces of the operators around the routed
+// experts: the scored router and its gradient (route_kernels.cu), 8-bit
+// quantisation of rows and 8-bit products (int8_kernels.cu, int8_gemm.cu).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "chord.h"
+#include "kernels.h"
+
+namespace chord {
+
+// chord_moe_route
+struct MoeRouteArgs {
+    const void* logits;  // [T, E], rows ld elements apart
+    int type;            // CHORD_TYPE_*
+    int64_t T;
+    int64_t ld;
+    int E;  // <= 1024
+    int k;  // <= 32
+    int scoring;
+    const float* bias;  // [E] or null
+    int n_group;        // <= 32, E % n_group == 0
+    int topk_group;
+    int group_top;  // 1 or 2
+    int renorm;
+    float scale;
+    int32_t* ids;
+    float* w;
+};
+cudaError_t launch_moe_route(const MoeRouteArgs& a, int sms, cudaStream_t s);
+
+// chord_moe_route_backward
+struct MoeRouteBwdArgs {
+    const float* d_w;
+    const void* logits;
+    int type;
+    int64_t T;
+    int64_t ld;
+    int E;
+    int k;
+    int scoring;
+    int renorm;
+    float scale;
+    const int32_t* ids;
+    const float* w;
+    void* d_logits;  // [T, E] packed, of `type`
+};
+cudaError_t launch_moe_route_backward(const MoeRouteBwdArgs& a, int sms, cudaStream_t s);
+
+// chord_int8_quantize / chord_int8_silu_mul_quantize
+struct QuantArgs {
+    const void* x;  // [T, K] (silu_mul: [T, 2K], gate then up), rows ld_x elements apart
+    int type;
+    int64_t T;
+    int K;
+    int64_t ld_x;
+    int8_t* q;  // [T, K], rows ld_q bytes apart, 16-byte aligned
+    int64_t ld_q;
+    float* scale;  // [T]
+    int silu_mul;
+    int* err;  // cleared by the first block, or null
+};
+cudaError_t launch_int8_quantize(const QuantArgs& a, int sms, cudaStream_t s);
+
+// chord_int8_matmul
+struct Int8Args {
+    const int8_t* a;  // [T, K] tokens, rows ld_a bytes apart
+    const int8_t* w;  // [N, K] channels, rows ld_w bytes apart
+    int64_t ld_a;
+    int64_t ld_w;
+    const float* a_scale;  // [T]
+    const float* w_scale;  // [N]
+    int64_t T;
+    int N;
+    int K;
+    const void* residual;  // [T, N] of `type`, rows ld_r elements apart, or null
+    int64_t ld_r;
+    void* out;  // [T, N] of `type`, rows ld_out elements apart
+    int64_t ld_out;
+    int type;
+    int* err;  // device error word, cleared by the first block, or null
+    int clear_err;
+};
+// CUDA-core product (any T; streams the weights once per 8 tokens)
+cudaError_t launch_int8_rows(const Int8Args& a, int sms, cudaStream_t s);
+
+// ---------------------------------------------------------------------------
+// element types
+// ---------------------------------------------------------------------------
+template <typename T>
+__device__ __forceinline__ float to_f32(T v);
+template <>
+__device__ __forceinline__ float to_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <>
+__device__ __forceinline__ float to_f32<__half>(__half v) { return __half2float(v); }
+
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+
+// f(T{}) for the element type a CHORD_TYPE_* names
+template <typename F>
+cudaError_t with_type(int type, F&& f)
+{
+    switch (type) {
+    case CHORD_TYPE_F32: return f(float{});
+    case CHORD_TYPE_BF16: return f(__nv_bfloat16{});
+    case CHORD_TYPE_F16: return f(__half{});
+    }
+    return cudaErrorInvalidValue;
+}
+inline int type_size(int type) { return type == CHORD_TYPE_F32 ? 4 : 2; }
+
+}  // namespace chord
