@@ -64,9 +64,12 @@ Scratch scratch(int64_t T, int K, int I)
     return p;
 }
 
-cudaError_t product(const Int8Args& a, const DeviceInfo& dev, cudaStream_t s)
+// after_quantize: a quantise kernel of the same call precedes the product
+cudaError_t product(const Int8Args& a, bool after_quantize, const DeviceInfo& dev, cudaStream_t s)
 {
-    return launch_int8_rows(a, dev.sms, s);
+    if (a.T <= 8)
+        return launch_int8_rows(a, dev.sms, s);
+    return launch_int8_gemm(a, after_quantize, dev.sms, s);
 }
 
 }  // namespace
@@ -194,7 +197,7 @@ chord_status chord_int8_matmul(const int8_t* a, int64_t ld_a, const float* a_sca
                      residual, ld_r, out,  ld_out, type,    static_cast<int*>(workspace), 1};
     PdlScope pdl(T <= kPdlMaxRows);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (product(g, dev, s) != cudaSuccess)
+    if (product(g, false, dev, s) != cudaSuccess)
         return CHORD_ERR_CUDA;
     return finish(flags, workspace, s);
 }
@@ -230,7 +233,7 @@ chord_status chord_int8_linear(const void* x, int type, int64_t ld_x, const int8
     const QuantArgs qa{x, type, T, K, ld_x, q, pad16(K), qs, 0, err};
     const Int8Args g{q,        w,    pad16(K), ld_w,   qs,   w_scale, T, N, K,
                      residual, ld_r, out,      ld_out, type, err,     0};
-    if (launch_int8_quantize(qa, dev.sms, s) != cudaSuccess || product(g, dev, s) != cudaSuccess)
+    if (launch_int8_quantize(qa, dev.sms, s) != cudaSuccess || product(g, true, dev, s) != cudaSuccess)
         return CHORD_ERR_CUDA;
     return finish(flags, workspace, s);
 }
@@ -275,8 +278,8 @@ chord_status chord_int8_mlp(const void* x, int type, int64_t ld_x, const int8_t*
     const QuantArgs ha{mid, CHORD_TYPE_F32, T, I, 2 * int64_t(I), q2, pad16(I), qs2, 1, nullptr};
     const Int8Args g2{q2,       w2,   pad16(I), ld_w2,  qs2,  w2_scale, T, H, I,
                       residual, ld_r, out,      ld_out, type, err,      0};
-    if (launch_int8_quantize(qa, dev.sms, s) != cudaSuccess || product(g1, dev, s) != cudaSuccess ||
-        launch_int8_quantize(ha, dev.sms, s) != cudaSuccess || product(g2, dev, s) != cudaSuccess)
+    if (launch_int8_quantize(qa, dev.sms, s) != cudaSuccess || product(g1, true, dev, s) != cudaSuccess ||
+        launch_int8_quantize(ha, dev.sms, s) != cudaSuccess || product(g2, true, dev, s) != cudaSuccess)
         return CHORD_ERR_CUDA;
     return finish(flags, workspace, s);
 }

@@ -88,6 +88,9 @@ struct Int8Args {
 };
 // CUDA-core product (any T; streams the weights once per 8 tokens)
 cudaError_t launch_int8_rows(const Int8Args& a, int sms, cudaStream_t s);
+// tensor-core product.  w_ready: the preceding kernel of the stream does not
+// write the weight and lets this one start early (see the quantise kernel)
+cudaError_t launch_int8_gemm(const Int8Args& a, int w_ready, int sms, cudaStream_t s);
 
 // ---------------------------------------------------------------------------
 // element types
