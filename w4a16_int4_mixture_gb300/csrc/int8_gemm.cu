@@ -5,22 +5,31 @@
 // which holds every 8-bit integer exactly.  A product of two codes is an
 // integer of at most 2^14, and a chain of 1024 of them stays an integer of at
 // most 2^24, which fp32 holds exactly in whatever order the tensor core adds.
-// Chains of 1024 (kChain K stages) alternate between two accumulators in tensor
+// Chains of 1024 (kChain items) alternate between two accumulators in tensor
 // memory; the epilogue warps add each finished one into 32-bit integers in
 // registers, so the sum over any K is the exact integer.
 //
-// D[128 channels, NT tokens] = W_tile[128, K] A_tile[NT, K]^T: the weight is the
-// M operand, converted into tensor memory, the tokens the N operand, converted
-// into shared memory.  Both arrive as raw 8-bit boxes by TMA, half the bytes of
-// a 16-bit operand, and are converted once per stage:
-//   warp 0       producer: one box of each operand per K stage of 128 codes
-//   warp 1       MMA issuer;  warp 2  owner of the tensor memory
-//   warps 4-11   converters, two per lane quadrant: code ^ 0x80 under the fp16
-//                exponent of 1024 is 1024 + 128 + code; subtracting 1152 is exact
-//                (1.25 instructions per code)
-//   warps 12-19  epilogue, two per lane quadrant (a half of the token columns each)
-// Split K: a weight with fewer tiles than SMs is cut along K over the CTAs of a
-// cluster; the integer partial sums meet in distributed shared memory.
+// D[128 * CG channels, nt tokens] = W_tile[128 * CG, K] A_tile[nt, K]^T: the
+// weight is the M operand, converted into tensor memory, the tokens the N
+// operand, converted into shared memory.  CG = 2: two CTAs of a cluster share a
+// tile (cta_group::2); each holds 128 channels and half of the tokens, so a
+// token is converted once for 256 channels, and shared memory, which bounds a
+// single CTA (the raw and converted token bytes pass it four times), is relieved.
+// Both operands arrive as raw 8-bit boxes by TMA, half the bytes of a 16-bit
+// operand, 128 codes deep; an item is 64 of them.
+//   warp 0       producer: one box of each operand per raw stage
+//   warp 1       MMA issuer (of the first CTA);  warp 2  owner of tensor memory
+//   converters   NG groups of four warps, one per lane quadrant.  A group
+//                converts whole items in turn, so that the latencies of one
+//                item (shared and tensor memory, fences, barriers) overlap the
+//                other groups' (all warps on every item ran at 1800 clocks per
+//                128 codes whatever the token tile: 536 us for 8192 x 7168 x
+//                4096).  code ^ 0x80 under the fp16 exponent of 1024 is 1024 +
+//                128 + code; subtracting 1152 is exact (1.25 instructions per
+//                code)
+//   epilogue     eight warps, two per lane quadrant (half of the columns each)
+// Split K (CG = 1): a weight with fewer tiles than SMs is cut along K over the
+// CTAs of a cluster; the integer partial sums meet in distributed shared memory.
 // Every wait is bounded (2 s): on expiry CHORD_DEVERR_TIMEOUT is recorded, every
 // role leaves its loop and tensor memory is freed.
 #include <cudaTypedefs.h>
@@ -32,48 +41,57 @@ namespace chord {
 
 namespace {
 
-constexpr int kBK = 128;     // codes of a K stage (one 128-byte swizzled row)
-constexpr int kChain = 8;    // K stages of an accumulation chain (1024 products)
-constexpr int kTileM = 128;  // channels of a tile
-constexpr int kConvWarps = 8;
+constexpr int kRawK = 128;   // codes of a raw stage (one 128-byte swizzled row)
+constexpr int kItemK = 64;   // codes of an item (one 128-byte swizzled fp16 row)
+constexpr int kChain = 16;   // items of an accumulation chain (1024 products)
+constexpr int kTileM = 128;  // channels of a CTA's tile
 constexpr int kEpiWarps = 8;
-constexpr int kEpiWarp0 = 12;
-constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 
 struct Int8Gemm {
     Int8Args p;
-    int nt;        // token tile: a multiple of 16, at most NTMAX
-    int n_tiles;   // channel tiles
+    int nt;        // token tile: a multiple of 16 (CG = 2: 32), at most NTMAX
+    int n_tiles;   // channel tiles (of 128 * CG)
     int units;     // channel tiles * token tiles
-    int split;     // CTAs of a cluster that share a unit along K
+    int split;     // CTAs of a cluster that share a unit along K (CG = 1)
     int w_ready;   // the weight may be read before the preceding kernel has ended
 };
 
-template <int NTMAX_, int RS_, int AS_>
+// CG CTAs per tile, token tile, raw stages, converted items, converter groups,
+// and the registers of a producer / converter / epilogue thread (0: as launched)
+template <int CG_, int NTMAX_, int RS_, int AS_, int NG_, int R0_ = 0, int RC_ = 0, int RE_ = 0>
 struct Int8Cfg {
-    static constexpr int NTMAX = NTMAX_;  // largest token tile
-    static constexpr int RS = RS_;        // raw stages in shared memory
-    static constexpr int AS = AS_;        // converted stages (TMEM and shared memory)
-    static constexpr int W_RAW = kTileM * kBK;
-    static constexpr int T_RAW = NTMAX * kBK;
-    static constexpr int B_REGION = NTMAX * 128;  // one 64-element column block of the tokens
-    static constexpr int B_STAGE = 2 * B_REGION;
+    static constexpr int CG = CG_;
+    static constexpr int NTMAX = NTMAX_;
+    static constexpr int RS = RS_;
+    static constexpr int AS = AS_;
+    static constexpr int NG = NG_;
+    static constexpr int R0 = R0_, RC = RC_, RE = RE_;
+    static constexpr int EPI_WARP0 = 4 + 4 * NG;
+    static constexpr int THREADS = 32 * (EPI_WARP0 + kEpiWarps);
+    static constexpr int ROWS = NTMAX / CG;  // token rows of a CTA
+    static constexpr int W_RAW = kTileM * kRawK;
+    static constexpr int T_RAW = ROWS * kRawK;
+    static constexpr int B_ITEM = ROWS * 128;
     static constexpr int OFF_W = 0;
     static constexpr int OFF_T = OFF_W + RS * W_RAW;
     static constexpr int OFF_B = OFF_T + RS * T_RAW;
-    static constexpr int OFF_BARS = OFF_B + AS * B_STAGE;
+    static constexpr int OFF_BARS = OFF_B + AS * B_ITEM;
     static constexpr int NBARS = 2 * RS + 2 * AS + 4 + 1;
     static constexpr int OFF_MISC = OFF_BARS + 8 * NBARS;
     static constexpr int SMEM = OFF_MISC + 16 + 1024;  // + alignment slack
-    static constexpr int A_COLS = kBK / 2;
+    static constexpr int A_COLS = kItemK / 2;
     static constexpr int D_COL0 = AS * A_COLS;
     static constexpr int TMEM_COLS = 512;
-    static_assert(NTMAX % 16 == 0 && NTMAX <= 256, "token tile");
+    static_assert(NTMAX % (16 * CG) == 0 && NTMAX <= 256, "token tile");
     static_assert(T_RAW % 1024 == 0, "swizzle atoms need 1024-byte alignment");
     static_assert(D_COL0 + 2 * NTMAX <= TMEM_COLS, "tensor memory budget");
     static_assert(SMEM <= 232448 && SMEM > 116 * 1024, "one CTA per SM");
+    static_assert(NG <= AS && NG <= 2 * RS, "a group never waits for an item of its own");
+    // what the warpgroups take may not exceed what the CTA was launched with
+    static constexpr int REGS = 65536 / THREADS / 8 * 8;
+    static_assert(R0 + NG * RC + 2 * RE <= (3 + NG) * REGS, "register shares");
     // (split K: the partial sums take the place of the raw stages)
-    static_assert(kTileM * NTMAX * 4 <= OFF_BARS, "partial sums");
+    static_assert(kTileM * NTMAX * 4 <= OFF_B || CG == 2, "partial sums");
 };
 
 // four 8-bit codes -> four fp16 (two registers), exact
@@ -102,6 +120,101 @@ __device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, uint32_t (&v)[8])
                  : "memory");
 }
 
+template <int N>
+__device__ __forceinline__ void set_regs_dec()
+{
+    if constexpr (N > 0)
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_regs_inc()
+{
+    if constexpr (N > 0)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// tensor memory of a CTA, or of a CTA pair (both CTAs call)
+template <int CG>
+__device__ __forceinline__ void tmem_alloc_cg(uint32_t slot, uint32_t ncols)
+{
+    if constexpr (CG == 1) {
+        tmem_alloc(slot, ncols);
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(ncols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+}
+template <int CG>
+__device__ __forceinline__ void tmem_dealloc_cg(uint32_t taddr, uint32_t ncols)
+{
+    if constexpr (CG == 1)
+        tmem_dealloc(taddr, ncols);
+    else
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+
+// An item's four K = 16 MMAs from one elected lane of a converged warp: A columns
+// a + 8 j, B 32-byte step j of the swizzled row.  accumulate = 0: the first
+// overwrites D.
+#define CHORD_INT8_MMA4(GROUP)                                                                            \
+    asm volatile(                                                                                         \
+        "{\n\t.reg .pred e, p0, pt;\n\t.reg .b32 bl, al;\n\t.reg .b64 bd;\n\t"                            \
+        "setp.ne.b32 p0, %5, 0;\n\tsetp.eq.b32 pt, 0, 0;\n\telect.sync _|e, 0xffffffff;\n\t"              \
+        "mov.b64 bd, {%2, %3};\n\t@e tcgen05.mma." GROUP ".kind::f16 [%0], [%1], bd, %4, p0;\n\t"         \
+        "add.u32 bl, %2, 2;\n\tmov.b64 bd, {bl, %3};\n\tadd.u32 al, %1, 8;\n\t"                            \
+        "@e tcgen05.mma." GROUP ".kind::f16 [%0], [al], bd, %4, pt;\n\t"                                  \
+        "add.u32 bl, %2, 4;\n\tmov.b64 bd, {bl, %3};\n\tadd.u32 al, %1, 16;\n\t"                           \
+        "@e tcgen05.mma." GROUP ".kind::f16 [%0], [al], bd, %4, pt;\n\t"                                  \
+        "add.u32 bl, %2, 6;\n\tmov.b64 bd, {bl, %3};\n\tadd.u32 al, %1, 24;\n\t"                           \
+        "@e tcgen05.mma." GROUP ".kind::f16 [%0], [al], bd, %4, pt;\n\t}" ::"r"(d),                       \
+        "r"(a), "r"(static_cast<uint32_t>(b_desc)), "r"(static_cast<uint32_t>(b_desc >> 32)), "r"(idesc), \
+        "r"(accumulate)                                                                                   \
+        : "memory")
+template <int CG>
+__device__ __forceinline__ void mma_item(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t accumulate)
+{
+    if constexpr (CG == 1)
+        CHORD_INT8_MMA4("cta_group::1");
+    else
+        CHORD_INT8_MMA4("cta_group::2");
+}
+#undef CHORD_INT8_MMA4
+
+// Arrives on `bar` (of both CTAs of a pair) when the MMAs issued so far are done.
+template <int CG>
+__device__ __forceinline__ void commit_elect(uint32_t bar)
+{
+    if constexpr (CG == 1)
+        mma_commit_elect(bar);
+    else
+        asm volatile(
+            "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+            "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+            "[%0], %1;\n\t}" ::"r"(bar),
+            "h"(static_cast<uint16_t>(3))
+            : "memory");
+}
+
+// Arrival on a barrier of the pair's first CTA.  What it announces stays in the
+// CTA that wrote it (each SM's tensor core reads its own shared and tensor
+// memory) and was completed there before (tcgen05.wait::st, fence.proxy.async),
+// so the arrival only has to order the MMA's issue: with release and acquire at
+// cluster scope, each a memory barrier of some 500 clocks, an item of the pair
+// took 800 clocks instead of %s.
+template <int CG>
+__device__ __forceinline__ void arrive_first(uint32_t bar)
+{
+    if constexpr (CG == 1) {
+        mbar_arrive(bar);
+    } else {
+        uint32_t ra;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(ra) : "r"(bar));
+        asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(ra) : "memory");
+    }
+}
+
 __device__ __forceinline__ uint32_t cluster_rank()
 {
     uint32_t r;
@@ -121,18 +234,42 @@ __device__ __forceinline__ int ld_cluster_s32(uint32_t addr, uint32_t rank)
     return v;
 }
 
-// out (one type) of one token and channel
+// out of one channel and the cols tokens from t0 on (at most 8, those below T).
+// Every load goes out before the first store, which may write the residual.
 template <typename T>
-__device__ __forceinline__ void store_sum(const Int8Args& a, int64_t t, int n, int sum, float ws)
+__device__ __forceinline__ void store_sums(const Int8Args& a, int64_t t0, int cols, int n, const int* sum, float ws)
 {
-    float v = static_cast<float>(sum) * a.a_scale[t] * ws;
-    if (a.residual)
-        v += to_f32<T>(static_cast<const T*>(a.residual)[t * a.ld_r + n]);
-    static_cast<T*>(a.out)[t * a.ld_out + n] = from_f32<T>(v);
+    const int64_t left = a.T - t0;
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < cols && i < left)
+            v[i] = a.a_scale[t0 + i];
+    if (a.residual) {
+        T r[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < cols && i < left)
+                r[i] = static_cast<const T*>(a.residual)[(t0 + i) * a.ld_r + n];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < cols && i < left)
+                v[i] = static_cast<float>(sum[i]) * v[i] * ws + to_f32<T>(r[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < cols && i < left)
+                v[i] = static_cast<float>(sum[i]) * v[i] * ws;
+    }
+    T* out = static_cast<T*>(a.out) + t0 * a.ld_out + n;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < cols && i < left)
+            out[i * a.ld_out] = from_f32<T>(v[i]);
 }
 
 template <class C, typename T>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(C::THREADS, 1)
     int8_gemm_kernel(const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap t_map,
                      const Int8Gemm g)
 {
@@ -142,7 +279,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* smem = smem_raw + (sbase - raw_u32);
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const int rank = g.split > 1 ? static_cast<int>(cluster_rank()) : 0;
+    const int cluster = C::CG * g.split;  // (one of the two is 1)
+    const int rank = cluster > 1 ? static_cast<int>(cluster_rank()) : 0;
 
     const uint32_t bar0 = sbase + C::OFF_BARS;
     auto raw_full = [&](int s) { return bar0 + 8u * s; };
@@ -159,15 +297,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::RS; ++s) {
             mbar_init(raw_full(s), 1);
-            mbar_init(raw_empty(s), kConvWarps);
+            mbar_init(raw_empty(s), 8);  // (the four warps of the groups of its two items)
         }
         for (int s = 0; s < C::AS; ++s) {
-            mbar_init(cv_full(s), kConvWarps);
+            mbar_init(cv_full(s), 4 * C::CG);
             mbar_init(cv_empty(s), 1);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(acc_full(s), 1);
-            mbar_init(acc_empty(s), kEpiWarps);
+            mbar_init(acc_empty(s), kEpiWarps * C::CG);
         }
         mbar_init(drain_bar, 1);
         *abort_flag = 0;
@@ -176,9 +314,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tensormap(&t_map);
     }
     if (warp == 2)
-        tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
+        tmem_alloc_cg<C::CG>(smem_u32(tmem_slot), C::TMEM_COLS);
     tc_fence_before();
     __syncthreads();
+    if constexpr (C::CG == 2)
+        cluster_sync_all();  // (the first CTA's barriers take the second one's arrivals)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     if (!g.w_ready)
@@ -187,155 +327,177 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (g.p.clear_err && blockIdx.x == 0 && threadIdx.x == 0)
         *err = 0;  // (a wait that expires sets it 2 s from now at the earliest)
 
-    const int KT = (g.p.K + kBK - 1) / kBK;
-    const int k0 = rank * KT / g.split, k1 = (rank + 1) * KT / g.split;  // this CTA's K stages
-    const int u0 = blockIdx.x / g.split, ustep = gridDim.x / g.split;
+    // this CTA's (or pair's) units and K stages
+    const int KT = (g.p.K + kRawK - 1) / kRawK;
+    const int krank = C::CG == 1 ? rank : 0;
+    const int k0 = krank * KT / g.split, k1 = (krank + 1) * KT / g.split;
+    const int u0 = blockIdx.x / cluster, ustep = gridDim.x / cluster;
+    const int my_units = u0 < g.units ? (g.units - 1 - u0) / ustep + 1 : 0;
+    const int unit_items = 2 * (k1 - k0);
     const int nt = g.nt;
+    const int rows = nt / C::CG;
     int issued = 0;  // raw stages whose copies were issued
 
-    if (warp == 0) {
-        // ------------------------------------------------------------- producer
-        const uint64_t pol_w = g.units > g.n_tiles ? policy_evict_last() : policy_evict_first();
-        const uint64_t pol_t = policy_evict_last();
-        const uint32_t bytes = C::W_RAW + nt * kBK;
-        bool ok = true;
-        // the weight boxes of the first stages go out while the preceding kernel
-        // still writes the tokens
-        int early = 0;
-        if (g.w_ready) {
-            if (u0 < g.units)
-                for (; early < C::RS && k0 + early < k1; ++early)
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(raw_full(early), bytes);
-                        tma_load_2d(sbase + C::OFF_W + early * C::W_RAW, &w_map, (k0 + early) * kBK,
-                                    u0 % g.n_tiles * kTileM, raw_full(early), pol_w);
-                    }
-            pdl_wait();
-        }
-        int it = 0;
-        for (int u = u0; u < g.units && ok; u += ustep) {
-            const int row_w = u % g.n_tiles * kTileM, row_t = u / g.n_tiles * nt;
-            for (int ks = k0; ks < k1; ++ks, ++it) {
-                const int s = it % C::RS;
-                if (!mbar_wait(raw_empty(s), ((it / C::RS) & 1) ^ 1, abort_flag, err)) {
-                    ok = false;
-                    break;
-                }
-                if (lane == 0) {
-                    if (it >= early) {
-                        mbar_arrive_expect_tx(raw_full(s), bytes);
-                        tma_load_2d(sbase + C::OFF_W + s * C::W_RAW, &w_map, ks * kBK, row_w, raw_full(s), pol_w);
-                    }
-                    tma_load_2d(sbase + C::OFF_T + s * C::T_RAW, &t_map, ks * kBK, row_t, raw_full(s), pol_t);
-                }
-                __syncwarp();
+    if (warp < 4) {
+        set_regs_dec<C::R0>();
+        if (warp == 0) {
+            // --------------------------------------------------------- producer
+            const uint64_t pol_w = g.units > g.n_tiles ? policy_evict_last() : policy_evict_first();
+            const uint64_t pol_t = policy_evict_last();
+            const uint32_t bytes = C::W_RAW + rows * kRawK;
+            const int row_w0 = C::CG == 2 ? rank * kTileM : 0, row_t0 = C::CG == 2 ? rank * rows : 0;
+            bool ok = true;
+            // the weight boxes of the first stages go out while the preceding kernel
+            // still writes the tokens
+            int early = 0;
+            if (g.w_ready) {
+                if (my_units > 0)
+                    for (; early < C::RS && k0 + early < k1; ++early)
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(raw_full(early), bytes);
+                            tma_load_2d(sbase + C::OFF_W + early * C::W_RAW, &w_map, (k0 + early) * kRawK,
+                                        u0 % g.n_tiles * (kTileM * C::CG) + row_w0, raw_full(early), pol_w);
+                        }
+                pdl_wait();
             }
-        }
-        issued = it > early ? it : early;
-    } else if (warp == 1) {
-        // ----------------------------------------------------------- MMA issuer
-        const uint32_t idesc = idesc_f16_f32(kTileM, nt);
-        int it = 0, pc = 0, any = 0;
-        bool ok = true;
-        for (int u = u0; u < g.units && ok; u += ustep) {
-            for (int c0 = k0; c0 < k1 && ok; c0 += kChain, ++pc) {
-                const int c1 = c0 + kChain < k1 ? c0 + kChain : k1;
-                const int acc = pc & 1;
-                if (!__all_sync(0xffffffffu, mbar_wait(acc_empty(acc), ((pc >> 1) & 1) ^ 1, abort_flag, err))) {
-                    ok = false;
-                    break;
-                }
-                for (int ks = c0; ks < c1; ++ks, ++it) {
-                    const int s = it % C::AS;
-                    if (!__all_sync(0xffffffffu, mbar_wait(cv_full(s), (it / C::AS) & 1, abort_flag, err))) {
+            int it = 0;
+            for (int u = u0; u < g.units && ok; u += ustep) {
+                const int row_w = u % g.n_tiles * (kTileM * C::CG) + row_w0, row_t = u / g.n_tiles * nt + row_t0;
+                for (int ks = k0; ks < k1; ++ks, ++it) {
+                    const int s = it % C::RS;
+                    if (!mbar_wait(raw_empty(s), ((it / C::RS) & 1) ^ 1, abort_flag, err)) {
                         ok = false;
                         break;
                     }
-                    tc_fence_after();
-                    mma_stage8<C::B_REGION / 16>(tmem + C::D_COL0 + acc * C::NTMAX, tmem + s * C::A_COLS,
-                                                 smem_desc_sw128(sbase + C::OFF_B + s * C::B_STAGE), idesc,
-                                                 ks != c0 ? 1u : 0u);
-                    any = 1;
-                    mma_commit_elect(cv_empty(s));
-                }
-                if (ok)
-                    mma_commit_elect(acc_full(acc));
-            }
-        }
-        if (!ok && any) {  // work in flight ends before tensor memory is freed
-            mma_commit_elect(drain_bar);
-            mbar_drain(drain_bar, 0);
-        }
-        __syncwarp();
-    } else if (warp >= 4 && warp < kEpiWarp0) {
-        // ------------------------------------------------------------ converters
-        const int cw = warp - 4, half = cw >> 2, q = warp & 3;
-        const int row = q * 32 + lane;
-        const int tid = threadIdx.x - 128;  // 0..255
-        const uint32_t tlane = static_cast<uint32_t>(q * 32) << 16;
-        const int pieces = nt * 8;  // 16-byte pieces of a token stage
-        int it = 0;
-        bool ok = true;
-        for (int u = u0; u < g.units && ok; u += ustep) {
-            for (int ks = k0; ks < k1; ++ks, ++it) {
-                const int rs = it % C::RS, s = it % C::AS;
-                if (!mbar_wait(raw_full(rs), (it / C::RS) & 1, abort_flag, err) ||
-                    !mbar_wait(cv_empty(s), ((it / C::AS) & 1) ^ 1, abort_flag, err)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                // 64 codes of one channel -> 32 TMEM columns of this lane
-                const uint8_t* wrow = smem + C::OFF_W + rs * C::W_RAW + row * 128;
-#pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    uint32_t o[16];
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const uint4 v = *reinterpret_cast<const uint4*>(
-                            wrow + (((half * 4 + p * 2 + c) ^ (row & 7)) << 4));
-                        codes_to_f16(v.x, o[8 * c], o[8 * c + 1]);
-                        codes_to_f16(v.y, o[8 * c + 2], o[8 * c + 3]);
-                        codes_to_f16(v.z, o[8 * c + 4], o[8 * c + 5]);
-                        codes_to_f16(v.w, o[8 * c + 6], o[8 * c + 7]);
+                    if (lane == 0) {
+                        if (it >= early) {
+                            mbar_arrive_expect_tx(raw_full(s), bytes);
+                            tma_load_2d(sbase + C::OFF_W + s * C::W_RAW, &w_map, ks * kRawK, row_w, raw_full(s),
+                                        pol_w);
+                        }
+                        tma_load_2d(sbase + C::OFF_T + s * C::T_RAW, &t_map, ks * kRawK, row_t, raw_full(s),
+                                    pol_t);
                     }
-                    tmem_st_x16(tmem + tlane + s * C::A_COLS + half * 32 + p * 16, o);
+                    __syncwarp();
                 }
-                // tokens: piece c of row r (16 codes) becomes two 16-byte pieces of the
-                // 128-byte swizzled fp16 row; lanes of the upper half write theirs in
-                // the other order, so that eight lanes cover all banks
-                const uint8_t* traw = smem + C::OFF_T + rs * C::T_RAW;
-                uint8_t* tb = smem + C::OFF_B + s * C::B_STAGE;
-#pragma unroll 2
-                for (int i = tid; i < pieces; i += 256) {
-                    const int r = i >> 3, c = i & 7;
-                    const uint4 v = *reinterpret_cast<const uint4*>(traw + r * 128 + ((c ^ (r & 7)) << 4));
-                    uint4 a, b;
-                    codes_to_f16(v.x, a.x, a.y);
-                    codes_to_f16(v.y, a.z, a.w);
-                    codes_to_f16(v.z, b.x, b.y);
-                    codes_to_f16(v.w, b.z, b.w);
-                    uint8_t* dst = tb + (c >> 2) * C::B_REGION + r * 128;
-                    const int p0 = ((c & 3) * 2) ^ (r & 7), sw = c >> 2;
-                    *reinterpret_cast<uint4*>(dst + ((p0 ^ sw) << 4)) = sw ? b : a;
-                    *reinterpret_cast<uint4*>(dst + ((p0 ^ sw ^ 1) << 4)) = sw ? a : b;
-                }
-                // reads of the raw stage before the next TMA into it, writes of the
-                // token stage before the MMA reads it
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(raw_empty(rs));
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(cv_full(s));
             }
+            issued = it > early ? it : early;
+        } else if (warp == 1 && (C::CG == 1 || rank == 0)) {
+            // ------------------------------------------------------- MMA issuer
+            const uint32_t idesc = idesc_f16_f32(kTileM * C::CG, nt);
+            int j = 0, pc = 0, any = 0;
+            bool ok = true;
+            for (int u = 0; u < my_units && ok; ++u) {
+                for (int c0 = 0; c0 < unit_items && ok; c0 += kChain, ++pc) {
+                    const int c1 = c0 + kChain < unit_items ? c0 + kChain : unit_items;
+                    const int acc = pc & 1;
+                    if (!__all_sync(0xffffffffu, mbar_wait(acc_empty(acc), ((pc >> 1) & 1) ^ 1,
+                                                                   abort_flag, err))) {
+                        ok = false;
+                        break;
+                    }
+                    for (int c = c0; c < c1; ++c, ++j) {
+                        const int s = j % C::AS;
+                        if (!__all_sync(0xffffffffu,
+                                        mbar_wait(cv_full(s), (j / C::AS) & 1, abort_flag, err))) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        mma_item<C::CG>(tmem + C::D_COL0 + acc * C::NTMAX, tmem + s * C::A_COLS,
+                                        smem_desc_sw128(sbase + C::OFF_B + s * C::B_ITEM), idesc,
+                                        c != c0 ? 1u : 0u);
+                        any = 1;
+                        commit_elect<C::CG>(cv_empty(s));
+                    }
+                    if (ok)
+                        commit_elect<C::CG>(acc_full(acc));
+                }
+            }
+            if (!ok && any) {  // work in flight ends before tensor memory is freed
+                commit_elect<C::CG>(drain_bar);
+                mbar_drain(drain_bar, 0);
+            }
+            __syncwarp();
         }
-    } else if (warp >= kEpiWarp0) {
+    } else if (warp < C::EPI_WARP0) {
+        // ------------------------------------------------------------ converters
+        set_regs_dec<C::RC>();
+        const int grp = (warp - 4) >> 2, q = warp & 3;
+        const int row = q * 32 + lane;
+        const uint32_t tlane = static_cast<uint32_t>(q * 32) << 16;
+        const int pieces = rows * 4;  // 16-byte raw pieces of an item's tokens
+        const int total = my_units * unit_items;
+        bool ok = true;
+        int j = grp;
+        for (; j < total; j += C::NG) {
+            const int rs = (j >> 1) % C::RS, s = j % C::AS, h = (j & 1) * 4;
+            if (!mbar_wait(raw_full(rs), ((j >> 1) / C::RS) & 1, abort_flag, err)) {
+                ok = false;
+                break;
+            }
+            // 64 codes of one channel -> 32 TMEM columns of this lane
+            const uint8_t* wrow = smem + C::OFF_W + rs * C::W_RAW + row * 128;
+            uint4 v[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                v[c] = *reinterpret_cast<const uint4*>(wrow + (((h + c) ^ (row & 7)) << 4));
+            if (!mbar_wait(cv_empty(s), ((j / C::AS) & 1) ^ 1, abort_flag, err)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                uint32_t o[16];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    codes_to_f16(v[2 * p + c].x, o[8 * c], o[8 * c + 1]);
+                    codes_to_f16(v[2 * p + c].y, o[8 * c + 2], o[8 * c + 3]);
+                    codes_to_f16(v[2 * p + c].z, o[8 * c + 4], o[8 * c + 5]);
+                    codes_to_f16(v[2 * p + c].w, o[8 * c + 6], o[8 * c + 7]);
+                }
+                tmem_st_x16(tmem + tlane + s * C::A_COLS + p * 16, o);
+            }
+            // tokens: piece c of row r (16 codes) becomes two 16-byte pieces of the
+            // 128-byte swizzled fp16 row.  Eight lanes take the four pieces of rows r
+            // and r + 4, the second row's in the other order: reads and writes cover
+            // all banks
+            const uint8_t* traw = smem + C::OFF_T + rs * C::T_RAW;
+            uint8_t* tb = smem + C::OFF_B + s * C::B_ITEM;
+#pragma unroll 2
+            for (int i = q * 32 + lane; i < pieces; i += 128) {
+                const int c = i & 3, r = ((i >> 2) & 1) * 4 + ((i >> 3) & 3) + (i >> 5) * 8;
+                const uint4 x = *reinterpret_cast<const uint4*>(traw + r * 128 + (((h + c) ^ (r & 7)) << 4));
+                uint4 a, b;
+                codes_to_f16(x.x, a.x, a.y);
+                codes_to_f16(x.y, a.z, a.w);
+                codes_to_f16(x.z, b.x, b.y);
+                codes_to_f16(x.w, b.z, b.w);
+                uint8_t* dst = tb + r * 128;
+                const int sw = (r >> 2) & 1, p0 = (2 * c) ^ (r & 7) ^ sw;
+                *reinterpret_cast<uint4*>(dst + (p0 << 4)) = sw ? b : a;
+                *reinterpret_cast<uint4*>(dst + ((p0 ^ 1) << 4)) = sw ? a : b;
+            }
+            // reads of the raw stage before the next TMA into it, writes of the
+            // token item before the MMA reads it
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(raw_empty(rs));
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                arrive_first<C::CG>(cv_full(s));
+        }
+        // (pair: the last arrivals from the first CTA's commits have landed)
+        if (C::CG == 2 && ok && j > grp)
+            mbar_wait(cv_empty((j - C::NG) % C::AS), ((j - C::NG) / C::AS) & 1, abort_flag, err);
+    } else {
         // -------------------------------------------------------------- epilogue
-        const int q = warp & 3, half = (warp - kEpiWarp0) >> 2;
+        set_regs_inc<C::RE>();
+        const int q = warp & 3, half = (warp - C::EPI_WARP0) >> 2;
         const uint32_t tlane = static_cast<uint32_t>(q * 32) << 16;
         const int ncol = nt / 2, col0 = half * ncol;  // (nt % 16 == 0: ncol % 8 == 0)
         if (g.w_ready)
@@ -344,14 +506,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         for (int u = u0; u < g.units && ok; u += ustep) {
             int sum[C::NTMAX / 2];
-            for (int c0 = k0; c0 < k1; c0 += kChain, ++pc) {
+            for (int c0 = 0; c0 < unit_items; c0 += kChain, ++pc) {
                 const int acc = pc & 1;
                 if (!mbar_wait(acc_full(acc), (pc >> 1) & 1, abort_flag, err)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const bool first = c0 == k0;
+                const bool first = c0 == 0;
 #pragma unroll
                 for (int j = 0; j < C::NTMAX / 2; j += 8) {
                     if (j < ncol) {
@@ -368,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(acc_empty(acc));
+                    arrive_first<C::CG>(acc_empty(acc));
             }
             if (!ok)
                 break;
@@ -381,14 +543,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (j < ncol)
                         part[(col0 + j) * kTileM + r] = sum[j];
             } else {
-                const int n = u % g.n_tiles * kTileM + r;
+                const int n = u % g.n_tiles * (kTileM * C::CG) + (C::CG == 2 ? rank * kTileM : 0) + r;
                 const int64_t t0 = static_cast<int64_t>(u / g.n_tiles) * nt + col0;
                 if (n < g.p.N) {
                     const float ws = g.p.w_scale[n];
 #pragma unroll
-                    for (int j = 0; j < C::NTMAX / 2; ++j)
+                    for (int j = 0; j < C::NTMAX / 2; j += 8)
                         if (j < ncol && t0 + j < g.p.T)
-                            store_sum<T>(g.p, t0 + j, n, sum[j], ws);
+                            store_sums<T>(g.p, t0 + j, 8, n, sum + j, ws);
                 }
             }
         }
@@ -403,27 +565,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_drain(raw_full(i % C::RS), (i / C::RS) & 1);
         __syncwarp();
     }
+    if constexpr (C::CG == 2)
+        cluster_sync_all();  // (neither CTA frees what the other's MMAs still use)
     if (warp == 2) {
         tc_fence_after();
-        tmem_dealloc(tmem, C::TMEM_COLS);
+        tmem_dealloc_cg<C::CG>(tmem, C::TMEM_COLS);
     }
-    if (g.split > 1) {
+    if (C::CG == 1 && g.split > 1) {
         // every CTA of the cluster finishes a share of the token columns
         __syncthreads();
         cluster_sync_all();
         pdl_wait();
-        const int u = u0;
-        const int n0 = u % g.n_tiles * kTileM;
-        const int64_t t0 = static_cast<int64_t>(u / g.n_tiles) * nt;
+        const int n0 = u0 % g.n_tiles * kTileM;
+        const int64_t t0 = static_cast<int64_t>(u0 / g.n_tiles) * nt;
         const int c0 = rank * nt / g.split, c1 = (rank + 1) * nt / g.split;
-        for (int i = threadIdx.x; i < (c1 - c0) * kTileM; i += kThreads) {
+        for (int i = threadIdx.x; i < (c1 - c0) * kTileM; i += C::THREADS) {
             const int col = c0 + i / kTileM, r = i % kTileM;
             const uint32_t at = sbase + 4u * (col * kTileM + r);
             int sum = 0;
             for (int k = 0; k < g.split; ++k)
                 sum += ld_cluster_s32(at, k);
             if (n0 + r < g.p.N && t0 + col < g.p.T)
-                store_sum<T>(g.p, t0 + col, n0 + r, sum, g.p.w_scale[n0 + r]);
+                store_sums<T>(g.p, t0 + col, 1, n0 + r, &sum, g.p.w_scale[n0 + r]);
         }
         cluster_sync_all();  // (the partial sums stay until every CTA has read them)
     }
@@ -456,7 +619,7 @@ cudaError_t codes_rows_map(const int8_t* p, int64_t n, int K, int64_t ld, int ro
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(n)};
     // (a single row has no distance: any multiple of 16 will do)
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld >= K ? ld : (K + 15) / 16 * 16)};
-    const cuuint32_t box[2] = {kBK, static_cast<cuuint32_t>(rows)}, es[2] = {1, 1};
+    const cuuint32_t box[2] = {kRawK, static_cast<cuuint32_t>(rows)}, es[2] = {1, 1};
     return encode(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(p), dims, strides, box, es,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
@@ -482,27 +645,29 @@ cudaError_t launch_cfg(Int8Gemm g, int sms, cudaStream_t s)
     }
     CUtensorMap wm, tm;
     if ((e = codes_rows_map(g.p.w, g.p.N, g.p.K, g.p.ld_w, kTileM, &wm)) != cudaSuccess ||
-        (e = codes_rows_map(g.p.a, g.p.T, g.p.K, g.p.ld_a, g.nt, &tm)) != cudaSuccess)
+        (e = codes_rows_map(g.p.a, g.p.T, g.p.K, g.p.ld_a, g.nt / C::CG, &tm)) != cudaSuccess)
         return e;
+    const int cluster = C::CG * g.split;
+    const int most = g.split > 1 ? g.units : sms / C::CG;  // clusters
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = g.split > 1 ? g.units * g.split : (g.units < sms ? g.units : sms);
-    cfg.blockDim = kThreads;
+    cfg.gridDim = cluster * (g.units < most ? g.units : most);
+    cfg.blockDim = C::THREADS;
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = g_launch_pdl ? 1 : 0;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = g.split;
+    attr[1].val.clusterDim.x = cluster;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = g.split > 1 ? 2 : 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, int8_gemm_kernel<C, T>, wm, tm, g);
 }
 
-using CfgT32 = Int8Cfg<32, 8, 4>;
-using CfgT128 = Int8Cfg<128, 4, 2>;
-using CfgT192 = Int8Cfg<192, 3, 2>;
+using CfgT32 = Int8Cfg<1, 32, 8, 8, 4>;
+using CfgT128 = Int8Cfg<1, 128, 4, 4, 3, 40, 64, 120>;
+using CfgP160 = Int8Cfg<2, 160, 5, 6, 3, 40, 64, 120>;
 
 template <typename T>
 cudaError_t launch_type(const Int8Args& a, int w_ready, int sms, cudaStream_t s)
@@ -510,36 +675,36 @@ cudaError_t launch_type(const Int8Args& a, int w_ready, int sms, cudaStream_t s)
     Int8Gemm g{};
     g.p = a;
     g.w_ready = w_ready;
-    g.n_tiles = (a.N + kTileM - 1) / kTileM;
-    // token tile: the whole batch where it fits one, else the width of 128..192
-    // whose rounds of units cost least
+    g.split = 1;
     const int64_t t16 = (a.T + 15) / 16 * 16;
-    if (t16 <= 192) {
+    const int KT = (a.K + kRawK - 1) / kRawK;
+    if (t16 <= 128) {
+        // one token tile, K cut until the SMs are used
         g.nt = static_cast<int>(t16);
-    } else {
-        int64_t best = INT64_MAX;
-        for (int nt = 192; nt >= 128; nt -= 16) {
-            const int64_t units = (a.T + nt - 1) / nt * g.n_tiles;
-            const int64_t cost = (units + sms - 1) / sms * (nt + 16);
-            if (cost < best) {
-                best = cost;
-                g.nt = nt;
-            }
+        g.n_tiles = g.units = (a.N + kTileM - 1) / kTileM;
+        while (g.split < 8 && g.units * g.split * 2 <= sms && KT >= 4 * g.split)
+            g.split *= 2;
+        if (g.nt <= 32)
+            return launch_cfg<CfgT32, T>(g, sms, s);
+        return launch_cfg<CfgT128, T>(g, sms, s);
+    }
+    // CTA pairs (N of their MMA is a multiple of 32); the token tile whose rounds
+    // of units cost least
+    g.n_tiles = (a.N + 2 * kTileM - 1) / (2 * kTileM);
+    int64_t best = INT64_MAX;
+    for (int nt = CfgP160::NTMAX; nt >= 96; nt -= 32) {
+        const int64_t units = (a.T + nt - 1) / nt * g.n_tiles;
+        const int64_t cost = (units + sms / 2 - 1) / (sms / 2) * (nt + 16);
+        if (cost < best) {
+            best = cost;
+            g.nt = nt;
         }
     }
     const int64_t units = (a.T + g.nt - 1) / g.nt * g.n_tiles;
     if (units > INT32_MAX)
         return cudaErrorInvalidValue;
     g.units = static_cast<int>(units);
-    const int KT = (a.K + kBK - 1) / kBK;
-    g.split = 1;
-    while (g.split < 8 && g.units * g.split * 2 <= sms && KT >= 4 * g.split)
-        g.split *= 2;
-    if (g.nt <= 32)
-        return launch_cfg<CfgT32, T>(g, sms, s);
-    if (g.nt <= 128)
-        return launch_cfg<CfgT128, T>(g, sms, s);
-    return launch_cfg<CfgT192, T>(g, sms, s);
+    return launch_cfg<CfgP160, T>(g, sms, s);
 }
 
 }  // namespace
