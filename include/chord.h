@@ -506,7 +506,8 @@ chord_status chord_int8_silu_mul_quantize(const void* gate_up, int type, int64_t
  *   residual  device [T, N] of `type`, rows ld_r elements apart, or NULL; may be
  *             `out` itself (same rows and ld)
  *   out       device [T, N] of `type`, rows ld_out elements apart
- *   workspace device, >= 256 bytes, 256-aligned (the device error word)
+ *   workspace device, >= chord_int8_matmul_workspace_size(T, K) bytes,
+ *             256-aligned (the device error word, and the tokens as fp16 codes)
  *   flags     0 or CHORD_FLAG_VALIDATE
  * Limits: 1 <= K <= 131071, N >= 1.  T = 0 is allowed.
  *
@@ -515,10 +516,11 @@ chord_status chord_int8_silu_mul_quantize(const void* gate_up, int type, int64_t
  *   g, u = the rows 0..I-1, I..2I-1 of w13 [2I, H] times quantised x [T, H];
  *   out = w2 [H, I] times quantised silu(g) * u, plus the residual (the routed
  *   experts' output); g and u stay in fp32.
- * Their workspace: chord_int8_workspace_size(T, K, 0) and (T, H, I) bytes (0 for
- * bad arguments).
+ * Their workspace: chord_int8_workspace_size(T, K, 0) and (T, H, I) bytes (the
+ * size queries return 0 for bad arguments).
  */
 size_t chord_int8_workspace_size(int64_t T, int K, int I);
+size_t chord_int8_matmul_workspace_size(int64_t T, int K);
 chord_status chord_int8_matmul(const int8_t* a, int64_t ld_a, const float* a_scale, const int8_t* w,
                                int64_t ld_w, const float* w_scale, int64_t T, int N, int K,
                                const void* residual, int64_t ld_r, void* out, int type,

@@ -82,6 +82,7 @@ SIGNATURES = {
     "chord_int8_quantize": (_int, [_vp, _int, _i64, _int, _i64, _vp, _i64, _vp, _vp]),
     "chord_int8_silu_mul_quantize": (_int, [_vp, _int, _i64, _int, _i64, _vp, _i64, _vp, _vp]),
     "chord_int8_workspace_size": (_sz, [_i64, _int, _int]),
+    "chord_int8_matmul_workspace_size": (_sz, [_i64, _int]),
     "chord_int8_matmul": (_int, [_vp, _i64, _vp, _vp, _i64, _vp, _i64, _int, _int, _vp, _i64, _vp,
                                  _int, _i64, _vp, _sz, _int, _vp]),
     "chord_int8_linear": (_int, [_vp, _int, _i64, _vp, _i64, _vp, _i64, _int, _int, _vp, _i64, _vp,

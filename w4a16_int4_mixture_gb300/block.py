@@ -211,7 +211,7 @@ def int8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale
     _vec(w_scale, "w_scale", dev, N)
     ld_r = _residual(residual, dev, out_dtype, (T, N))
     out, ld_out = _output(out, dev, out_dtype, (T, N))
-    ws = _workspace(workspace, dev, 256)
+    ws = _workspace(workspace, dev, ops.lib().chord_int8_matmul_workspace_size(T, K))
     st = ops.lib().chord_int8_matmul(ops._p(a), ld_a, ops._p(a_scale), ops._p(w), ld_w,
                                      ops._p(w_scale), T, N, K, ops._p(residual), ld_r, ops._p(out),
                                      _TYPES[out_dtype], ld_out, ops._p(ws), ws.numel(), flags,

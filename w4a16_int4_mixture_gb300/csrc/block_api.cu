@@ -41,6 +41,10 @@ chord_status finish(int flags, void* ws, cudaStream_t s)
     return chord_get_device_error(ws, nullptr, 0, s);
 }
 
+// bytes of a token code between the kernels: 1, or 2 as the fp16 operand of the
+// tensor-core product
+int code_size(int64_t T) { return T <= kInt8RowsMaxT ? 1 : 2; }
+
 struct Scratch {  // of chord_int8_linear and chord_int8_mlp
     size_t codes, scales, mid, codes2, scales2, total;
 };
@@ -53,23 +57,34 @@ Scratch scratch(int64_t T, int K, int I)
         at += align_up(bytes);
         return r;
     };
-    p.codes = take(static_cast<size_t>(T) * pad16(K));
+    p.codes = take(static_cast<size_t>(T) * pad16(K) * code_size(T));
     p.scales = take(static_cast<size_t>(T) * 4);
     if (I > 0) {
         p.mid = take(static_cast<size_t>(T) * 2 * I * 4);
-        p.codes2 = take(static_cast<size_t>(T) * pad16(I));
+        p.codes2 = take(static_cast<size_t>(T) * pad16(I) * code_size(T));
         p.scales2 = take(static_cast<size_t>(T) * 4);
     }
     p.total = at;
     return p;
 }
 
-// after_quantize: a quantise kernel of the same call precedes the product
-cudaError_t product(const Int8Args& a, bool after_quantize, const DeviceInfo& dev, cudaStream_t s)
+// Quantises x (or silu(gate) * up of it) into `codes` and `scales`, in the form
+// the product of T tokens takes, and multiplies.
+cudaError_t quantize_product(QuantArgs q, Int8Args g, void* codes, float* scales, const DeviceInfo& dev,
+                             cudaStream_t s)
 {
-    if (a.T <= 8)
-        return launch_int8_rows(a, dev.sms, s);
-    return launch_int8_gemm(a, after_quantize, dev.sms, s);
+    const bool rows = g.T <= kInt8RowsMaxT;
+    q.q = rows ? static_cast<int8_t*>(codes) : nullptr;
+    q.q16 = rows ? nullptr : static_cast<__half*>(codes);
+    q.ld_q = g.ld_a = pad16(g.K);
+    q.scale = scales;
+    g.a = q.q;
+    g.a16 = q.q16;
+    g.a_scale = scales;
+    const cudaError_t e = launch_int8_quantize(q, dev.sms, s);
+    if (e != cudaSuccess)
+        return e;
+    return rows ? launch_int8_rows(g, dev.sms, s) : launch_int8_gemm(g, dev.sms, s);
 }
 
 }  // namespace
@@ -146,7 +161,7 @@ static chord_status quantize(const void* x, int type, int64_t T, int K, int64_t 
     chord_status st = device_info(&dev);
     if (st != CHORD_OK)
         return st;
-    const QuantArgs a{x, type, T, K, ld_x, q, ld_q, scale, silu_mul, nullptr};
+    const QuantArgs a{x, type, T, K, ld_x, q, nullptr, ld_q, scale, silu_mul, nullptr};
     PdlScope pdl(T <= kPdlMaxRows);
     return from_cuda(launch_int8_quantize(a, dev.sms, static_cast<cudaStream_t>(stream)));
 }
@@ -171,6 +186,13 @@ size_t chord_int8_workspace_size(int64_t T, int K, int I)
     return scratch(T, K, I).total;
 }
 
+size_t chord_int8_matmul_workspace_size(int64_t T, int K)
+{
+    if (T < 0 || !sizes_ok(T, 1, K))
+        return 0;
+    return kHeader + (T <= kInt8RowsMaxT ? 0 : align_up(static_cast<size_t>(T) * pad16(K) * 2));
+}
+
 chord_status chord_int8_matmul(const int8_t* a, int64_t ld_a, const float* a_scale, const int8_t* w,
                                int64_t ld_w, const float* w_scale, int64_t T, int N, int K,
                                const void* residual, int64_t ld_r, void* out, int type,
@@ -187,17 +209,28 @@ chord_status chord_int8_matmul(const int8_t* a, int64_t ld_a, const float* a_sca
         return CHORD_OK;
     if (!a || !a_scale || !w || !w_scale || !out || !aligned16(a) || !aligned16(w))
         return CHORD_ERR_INVALID_ARG;
-    chord_status st = check_ws(workspace, workspace_bytes, kHeader);
+    chord_status st = check_ws(workspace, workspace_bytes, chord_int8_matmul_workspace_size(T, K));
     if (st != CHORD_OK)
         return st;
     DeviceInfo dev;
     if ((st = device_info(&dev)) != CHORD_OK)
         return st;
-    const Int8Args g{a,        w,    ld_a, ld_w,   a_scale, w_scale, T, N, K,
-                     residual, ld_r, out,  ld_out, type,    static_cast<int*>(workspace), 1};
+    Int8Args g{a, nullptr, w, ld_a, ld_w, a_scale, w_scale, T, N, K, residual, ld_r, out, ld_out, type,
+               static_cast<int*>(workspace)};
     PdlScope pdl(T <= kPdlMaxRows);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (product(g, false, dev, s) != cudaSuccess)
+    cudaError_t e = cudaSuccess;
+    if (T <= kInt8RowsMaxT) {
+        e = launch_int8_rows(g, dev.sms, s);
+    } else {
+        __half* a16 = reinterpret_cast<__half*>(static_cast<uint8_t*>(workspace) + kHeader);
+        e = launch_int8_to_f16(a, ld_a, T, K, a16, pad16(K), g.err, dev.sms, s);
+        g.a16 = a16;
+        g.ld_a = pad16(K);
+        if (e == cudaSuccess)
+            e = launch_int8_gemm(g, dev.sms, s);
+    }
+    if (e != cudaSuccess)
         return CHORD_ERR_CUDA;
     return finish(flags, workspace, s);
 }
@@ -226,14 +259,12 @@ chord_status chord_int8_linear(const void* x, int type, int64_t ld_x, const int8
         return st;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     int* err = static_cast<int*>(workspace);
-    int8_t* q = reinterpret_cast<int8_t*>(ws + p.codes);
     float* qs = reinterpret_cast<float*>(ws + p.scales);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     PdlScope pdl(T <= kPdlMaxRows);
-    const QuantArgs qa{x, type, T, K, ld_x, q, pad16(K), qs, 0, err};
-    const Int8Args g{q,        w,    pad16(K), ld_w,   qs,   w_scale, T, N, K,
-                     residual, ld_r, out,      ld_out, type, err,     0};
-    if (launch_int8_quantize(qa, dev.sms, s) != cudaSuccess || product(g, true, dev, s) != cudaSuccess)
+    const QuantArgs qa{x, type, T, K, ld_x, nullptr, nullptr, 0, nullptr, 0, err};
+    const Int8Args g{nullptr, nullptr, w, 0, ld_w, nullptr, w_scale, T, N, K, residual, ld_r, out, ld_out, type, err};
+    if (quantize_product(qa, g, ws + p.codes, qs, dev, s) != cudaSuccess)
         return CHORD_ERR_CUDA;
     return finish(flags, workspace, s);
 }
@@ -263,23 +294,21 @@ chord_status chord_int8_mlp(const void* x, int type, int64_t ld_x, const int8_t*
         return st;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     int* err = static_cast<int*>(workspace);
-    int8_t* q = reinterpret_cast<int8_t*>(ws + p.codes);
     float* qs = reinterpret_cast<float*>(ws + p.scales);
-    float* mid = reinterpret_cast<float*>(ws + p.mid);
-    int8_t* q2 = reinterpret_cast<int8_t*>(ws + p.codes2);
     float* qs2 = reinterpret_cast<float*>(ws + p.scales2);
+    float* mid = reinterpret_cast<float*>(ws + p.mid);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     PdlScope pdl(T <= kPdlMaxRows);
     // gate and up stay in fp32 between the products: rounding them to 16 bits
     // would move codes of the second quantisation
-    const QuantArgs qa{x, type, T, H, ld_x, q, pad16(H), qs, 0, err};
-    const Int8Args g1{q,       w13, pad16(H), ld_w13,         qs,             w13_scale, T, 2 * I, H,
-                      nullptr, 0,   mid,      2 * int64_t(I), CHORD_TYPE_F32, err,       0};
-    const QuantArgs ha{mid, CHORD_TYPE_F32, T, I, 2 * int64_t(I), q2, pad16(I), qs2, 1, nullptr};
-    const Int8Args g2{q2,       w2,   pad16(I), ld_w2,  qs2,  w2_scale, T, H, I,
-                      residual, ld_r, out,      ld_out, type, err,      0};
-    if (launch_int8_quantize(qa, dev.sms, s) != cudaSuccess || product(g1, true, dev, s) != cudaSuccess ||
-        launch_int8_quantize(ha, dev.sms, s) != cudaSuccess || product(g2, true, dev, s) != cudaSuccess)
+    const int64_t ld_m = 2 * static_cast<int64_t>(I);
+    const QuantArgs xa{x, type, T, H, ld_x, nullptr, nullptr, 0, nullptr, 0, err};
+    const Int8Args g1{nullptr, nullptr, w13, 0,   ld_w13, nullptr,        w13_scale, T, 2 * I, H,
+                      nullptr, 0,       mid, ld_m, CHORD_TYPE_F32, err};
+    const QuantArgs ha{mid, CHORD_TYPE_F32, T, I, ld_m, nullptr, nullptr, 0, nullptr, 1, nullptr};
+    const Int8Args g2{nullptr, nullptr, w2, 0, ld_w2, nullptr, w2_scale, T, H, I, residual, ld_r, out, ld_out, type, err};
+    if (quantize_product(xa, g1, ws + p.codes, qs, dev, s) != cudaSuccess ||
+        quantize_product(ha, g2, ws + p.codes2, qs2, dev, s) != cudaSuccess)
         return CHORD_ERR_CUDA;
     return finish(flags, workspace, s);
 }

@@ -59,18 +59,20 @@ struct QuantArgs {
     int64_t T;
     int K;
     int64_t ld_x;
-    int8_t* q;  // [T, K], rows ld_q bytes apart, 16-byte aligned
+    int8_t* q;    // [T, K], rows ld_q codes apart, 16-byte aligned, or null:
+    __half* q16;  // the same codes as fp16 (exact), for the tensor-core product
     int64_t ld_q;
     float* scale;  // [T]
     int silu_mul;
-    int* err;  // cleared by the first block, or null
+    int* err;  // device error word to clear, or null
 };
 cudaError_t launch_int8_quantize(const QuantArgs& a, int sms, cudaStream_t s);
 
 // chord_int8_matmul
 struct Int8Args {
-    const int8_t* a;  // [T, K] tokens, rows ld_a bytes apart
-    const int8_t* w;  // [N, K] channels, rows ld_w bytes apart
+    const int8_t* a;    // [T, K] tokens, rows ld_a codes apart (CUDA-core product)
+    const __half* a16;  // the same codes as fp16 (tensor-core product)
+    const int8_t* w;    // [N, K] channels, rows ld_w bytes apart
     int64_t ld_a;
     int64_t ld_w;
     const float* a_scale;  // [T]
@@ -83,14 +85,20 @@ struct Int8Args {
     void* out;  // [T, N] of `type`, rows ld_out elements apart
     int64_t ld_out;
     int type;
-    int* err;  // device error word, cleared by the first block, or null
-    int clear_err;
+    int* err;  // device error word (the call's first kernel clears it)
 };
+// 8-bit codes [T, K], rows ld_a apart, as fp16, rows ld_out apart (multiples of 16)
+cudaError_t launch_int8_to_f16(const int8_t* a, int64_t ld_a, int64_t T, int K, __half* out, int64_t ld_out,
+                               int* err, int sms, cudaStream_t s);
+// Up to this many tokens the CUDA-core product is taken.
+constexpr int64_t kInt8RowsMaxT = 8;
 // CUDA-core product (any T; streams the weights once per 8 tokens)
 cudaError_t launch_int8_rows(const Int8Args& a, int sms, cudaStream_t s);
-// tensor-core product.  w_ready: the preceding kernel of the stream does not
-// write the weight and lets this one start early (see the quantise kernel)
-cudaError_t launch_int8_gemm(const Int8Args& a, int w_ready, int sms, cudaStream_t s);
+// Tensor-core product of a.a16.  The kernel before it in the stream must be one
+// of those above that make the codes: it does not write the weight and lets its
+// successor start only after its own predecessors have ended, so this one reads
+// the weight before that kernel has ended.
+cudaError_t launch_int8_gemm(const Int8Args& a, int sms, cudaStream_t s);
 
 // ---------------------------------------------------------------------------
 // element types

@@ -11,22 +11,22 @@
 //
 // D[128 * CG channels, nt tokens] = W_tile[128 * CG, K] A_tile[nt, K]^T: the
 // weight is the M operand, converted into tensor memory, the tokens the N
-// operand, converted into shared memory.  CG = 2: two CTAs of a cluster share a
-// tile (cta_group::2); each holds 128 channels and half of the tokens, so a
-// token is converted once for 256 channels, and shared memory, which bounds a
-// single CTA (the raw and converted token bytes pass it four times), is relieved.
-// Both operands arrive as raw 8-bit boxes by TMA, half the bytes of a 16-bit
-// operand, 128 codes deep; an item is 64 of them.
-//   warp 0       producer: one box of each operand per raw stage
+// operand, in shared memory.  Weights arrive as raw 8-bit boxes by TMA and are
+// converted here, once per tile; tokens come as fp16 codes, which the quantise
+// kernel writes (or chord_int8_matmul's first kernel makes of 8-bit ones) once
+// for all channel tiles: converting them here as well took a third of the
+// converters' time (8192 x 7168 x 4096: 396 us against %TOK).  CG = 2: two CTAs
+// of a cluster share a tile (cta_group::2); each holds 128 channels and half of
+// the tokens.  A raw stage is 128 codes deep, an item 64 of them.
+//   warp 0       weight producer: a TMA box per raw stage
 //   warp 1       MMA issuer (of the first CTA);  warp 2  owner of tensor memory
+//   warp 3       token producer: a TMA box per item
 //   converters   NG groups of four warps, one per lane quadrant.  A group
 //                converts whole items in turn, so that the latencies of one
 //                item (shared and tensor memory, fences, barriers) overlap the
-//                other groups' (all warps on every item ran at 1800 clocks per
-//                128 codes whatever the token tile: 536 us for 8192 x 7168 x
-//                4096).  code ^ 0x80 under the fp16 exponent of 1024 is 1024 +
-//                128 + code; subtracting 1152 is exact (1.25 instructions per
-//                code)
+//                other groups'.  code ^ 0x80 under the fp16 exponent of 1024 is
+//                1024 + 128 + code; subtracting 1152 is exact (1.25
+//                instructions per code)
 //   epilogue     eight warps, two per lane quadrant (half of the columns each)
 // Split K (CG = 1): a weight with fewer tiles than SMs is cut along K over the
 // CTAs of a cluster; the integer partial sums meet in distributed shared memory.
@@ -53,11 +53,11 @@ struct Int8Gemm {
     int n_tiles;   // channel tiles (of 128 * CG)
     int units;     // channel tiles * token tiles
     int split;     // CTAs of a cluster that share a unit along K (CG = 1)
-    int w_ready;   // the weight may be read before the preceding kernel has ended
 };
 
-// CG CTAs per tile, token tile, raw stages, converted items, converter groups,
-// and the registers of a producer / converter / epilogue thread (0: as launched)
+// CG CTAs per tile, token tile, raw weight stages, items in flight (weights in
+// tensor memory, tokens in shared memory: one ring), converter groups, and the
+// registers of a producer / converter / epilogue thread (0: as launched)
 template <int CG_, int NTMAX_, int RS_, int AS_, int NG_, int R0_ = 0, int RC_ = 0, int RE_ = 0>
 struct Int8Cfg {
     static constexpr int CG = CG_;
@@ -70,28 +70,26 @@ struct Int8Cfg {
     static constexpr int THREADS = 32 * (EPI_WARP0 + kEpiWarps);
     static constexpr int ROWS = NTMAX / CG;  // token rows of a CTA
     static constexpr int W_RAW = kTileM * kRawK;
-    static constexpr int T_RAW = ROWS * kRawK;
     static constexpr int B_ITEM = ROWS * 128;
     static constexpr int OFF_W = 0;
-    static constexpr int OFF_T = OFF_W + RS * W_RAW;
-    static constexpr int OFF_B = OFF_T + RS * T_RAW;
+    static constexpr int OFF_B = OFF_W + RS * W_RAW;
     static constexpr int OFF_BARS = OFF_B + AS * B_ITEM;
-    static constexpr int NBARS = 2 * RS + 2 * AS + 4 + 1;
+    static constexpr int NBARS = 2 * RS + 3 * AS + 4 + 1;
     static constexpr int OFF_MISC = OFF_BARS + 8 * NBARS;
     static constexpr int SMEM = OFF_MISC + 16 + 1024;  // + alignment slack
     static constexpr int A_COLS = kItemK / 2;
     static constexpr int D_COL0 = AS * A_COLS;
     static constexpr int TMEM_COLS = 512;
     static_assert(NTMAX % (16 * CG) == 0 && NTMAX <= 256, "token tile");
-    static_assert(T_RAW % 1024 == 0, "swizzle atoms need 1024-byte alignment");
+    static_assert(B_ITEM % 1024 == 0, "swizzle atoms need 1024-byte alignment");
     static_assert(D_COL0 + 2 * NTMAX <= TMEM_COLS, "tensor memory budget");
     static_assert(SMEM <= 232448 && SMEM > 116 * 1024, "one CTA per SM");
     static_assert(NG <= AS && NG <= 2 * RS, "a group never waits for an item of its own");
     // what the warpgroups take may not exceed what the CTA was launched with
     static constexpr int REGS = 65536 / THREADS / 8 * 8;
     static_assert(R0 + NG * RC + 2 * RE <= (3 + NG) * REGS, "register shares");
-    // (split K: the partial sums take the place of the raw stages)
-    static_assert(kTileM * NTMAX * 4 <= OFF_B || CG == 2, "partial sums");
+    // (split K: the partial sums take the place of the stages)
+    static_assert(kTileM * NTMAX * 4 <= OFF_BARS, "partial sums");
 };
 
 // four 8-bit codes -> four fp16 (two registers), exact
@@ -234,38 +232,60 @@ __device__ __forceinline__ int ld_cluster_s32(uint32_t addr, uint32_t rank)
     return v;
 }
 
-// out of one channel and the cols tokens from t0 on (at most 8, those below T).
-// Every load goes out before the first store, which may write the residual.
 template <typename T>
+__device__ __forceinline__ void store_sum(const Int8Args& a, int64_t t, int n, int sum, float ws)
+{
+    float v = static_cast<float>(sum) * a.a_scale[t] * ws;
+    if (a.residual)
+        v += to_f32<T>(static_cast<const T*>(a.residual)[t * a.ld_r + n]);
+    static_cast<T*>(a.out)[t * a.ld_out + n] = from_f32<T>(v);
+}
+
+// out of one channel and 8 * NB tokens from t0 on (those below T, at most cols).
+// The loads of a batch of 8 go out before the stores of the batch before it,
+// which may write the residual: one at a time, each token waited for its own.
+template <typename T, int NB>
 __device__ __forceinline__ void store_sums(const Int8Args& a, int64_t t0, int cols, int n, const int* sum, float ws)
 {
-    const int64_t left = a.T - t0;
-    float v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < cols && i < left)
-            v[i] = a.a_scale[t0 + i];
-    if (a.residual) {
-        T r[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < cols && i < left)
-                r[i] = static_cast<const T*>(a.residual)[(t0 + i) * a.ld_r + n];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < cols && i < left)
-                v[i] = static_cast<float>(sum[i]) * v[i] * ws + to_f32<T>(r[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < cols && i < left)
-                v[i] = static_cast<float>(sum[i]) * v[i] * ws;
-    }
+    const int lim = a.T - t0 < cols ? static_cast<int>(a.T - t0) : cols;
+    const T* res = static_cast<const T*>(a.residual) + t0 * a.ld_r + n;
     T* out = static_cast<T*>(a.out) + t0 * a.ld_out + n;
+    const float* as = a.a_scale + t0;
+    T r[2][8];
+    auto load = [&](int b) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < cols && i < left)
-            out[i * a.ld_out] = from_f32<T>(v[i]);
+        for (int i = 0; i < 8; ++i)
+            if (8 * b + i < lim)
+                r[b & 1][i] = res[(8 * b + i) * a.ld_r];
+    };
+    if (a.residual)
+        load(0);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        if (8 * b < lim) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (8 * b + i < lim)
+                    v[i] = as[8 * b + i];
+            if (a.residual && b + 1 < NB)
+                load(b + 1);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (8 * b + i < lim)
+                    v[i] = static_cast<float>(sum[8 * b + i]) * v[i] * ws;
+            if (a.residual) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (8 * b + i < lim)
+                        v[i] += to_f32<T>(r[b & 1][i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (8 * b + i < lim)
+                    out[(8 * b + i) * a.ld_out] = from_f32<T>(v[i]);
+        }
+    }
 }
 
 template <class C, typename T>
@@ -285,10 +305,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     const uint32_t bar0 = sbase + C::OFF_BARS;
     auto raw_full = [&](int s) { return bar0 + 8u * s; };
     auto raw_empty = [&](int s) { return bar0 + 8u * (C::RS + s); };
-    auto cv_full = [&](int s) { return bar0 + 8u * (2 * C::RS + s); };
-    auto cv_empty = [&](int s) { return bar0 + 8u * (2 * C::RS + C::AS + s); };
-    auto acc_full = [&](int s) { return bar0 + 8u * (2 * C::RS + 2 * C::AS + s); };
-    auto acc_empty = [&](int s) { return bar0 + 8u * (2 * C::RS + 2 * C::AS + 2 + s); };
+    auto tok_full = [&](int s) { return bar0 + 8u * (2 * C::RS + s); };
+    auto cv_full = [&](int s) { return bar0 + 8u * (2 * C::RS + C::AS + s); };
+    auto cv_empty = [&](int s) { return bar0 + 8u * (2 * C::RS + 2 * C::AS + s); };
+    auto acc_full = [&](int s) { return bar0 + 8u * (2 * C::RS + 3 * C::AS + s); };
+    auto acc_empty = [&](int s) { return bar0 + 8u * (2 * C::RS + 3 * C::AS + 2 + s); };
     const uint32_t drain_bar = bar0 + 8u * (C::NBARS - 1);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
@@ -300,6 +321,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             mbar_init(raw_empty(s), 8);  // (the four warps of the groups of its two items)
         }
         for (int s = 0; s < C::AS; ++s) {
+            mbar_init(tok_full(s), 1);
             mbar_init(cv_full(s), 4 * C::CG);
             mbar_init(cv_empty(s), 1);
         }
@@ -321,11 +343,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         cluster_sync_all();  // (the first CTA's barriers take the second one's arrivals)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    if (!g.w_ready)
-        pdl_wait();
     pdl_launch_dependents();
-    if (g.p.clear_err && blockIdx.x == 0 && threadIdx.x == 0)
-        *err = 0;  // (a wait that expires sets it 2 s from now at the earliest)
 
     // this CTA's (or pair's) units and K stages
     const int KT = (g.p.K + kRawK - 1) / kRawK;
@@ -336,33 +354,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     const int unit_items = 2 * (k1 - k0);
     const int nt = g.nt;
     const int rows = nt / C::CG;
-    int issued = 0;  // raw stages whose copies were issued
+    int issued = 0;  // weight / token producer: stages whose copies were issued
 
     if (warp < 4) {
         set_regs_dec<C::R0>();
         if (warp == 0) {
-            // --------------------------------------------------------- producer
-            const uint64_t pol_w = g.units > g.n_tiles ? policy_evict_last() : policy_evict_first();
-            const uint64_t pol_t = policy_evict_last();
-            const uint32_t bytes = C::W_RAW + rows * kRawK;
-            const int row_w0 = C::CG == 2 ? rank * kTileM : 0, row_t0 = C::CG == 2 ? rank * rows : 0;
+            // -------------------------------------------------- weight producer
+            const uint64_t pol = g.units > g.n_tiles ? policy_evict_last() : policy_evict_first();
+            const int row0 = C::CG == 2 ? rank * kTileM : 0;
             bool ok = true;
-            // the weight boxes of the first stages go out while the preceding kernel
-            // still writes the tokens
-            int early = 0;
-            if (g.w_ready) {
-                if (my_units > 0)
-                    for (; early < C::RS && k0 + early < k1; ++early)
-                        if (lane == 0) {
-                            mbar_arrive_expect_tx(raw_full(early), bytes);
-                            tma_load_2d(sbase + C::OFF_W + early * C::W_RAW, &w_map, (k0 + early) * kRawK,
-                                        u0 % g.n_tiles * (kTileM * C::CG) + row_w0, raw_full(early), pol_w);
-                        }
-                pdl_wait();
-            }
             int it = 0;
             for (int u = u0; u < g.units && ok; u += ustep) {
-                const int row_w = u % g.n_tiles * (kTileM * C::CG) + row_w0, row_t = u / g.n_tiles * nt + row_t0;
+                const int row = u % g.n_tiles * (kTileM * C::CG) + row0;
                 for (int ks = k0; ks < k1; ++ks, ++it) {
                     const int s = it % C::RS;
                     if (!mbar_wait(raw_empty(s), ((it / C::RS) & 1) ^ 1, abort_flag, err)) {
@@ -370,18 +373,37 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         break;
                     }
                     if (lane == 0) {
-                        if (it >= early) {
-                            mbar_arrive_expect_tx(raw_full(s), bytes);
-                            tma_load_2d(sbase + C::OFF_W + s * C::W_RAW, &w_map, ks * kRawK, row_w, raw_full(s),
-                                        pol_w);
-                        }
-                        tma_load_2d(sbase + C::OFF_T + s * C::T_RAW, &t_map, ks * kRawK, row_t, raw_full(s),
-                                    pol_t);
+                        mbar_arrive_expect_tx(raw_full(s), C::W_RAW);
+                        tma_load_2d(sbase + C::OFF_W + s * C::W_RAW, &w_map, ks * kRawK, row, raw_full(s), pol);
                     }
                     __syncwarp();
                 }
             }
-            issued = it > early ? it : early;
+            issued = it;
+        } else if (warp == 3) {
+            // --------------------------------------------------- token producer
+            pdl_wait();  // (the weights are under way while the tokens are still written)
+            const uint64_t pol = policy_evict_last();
+            const uint32_t bytes = rows * 128;
+            const int row0 = C::CG == 2 ? rank * rows : 0;
+            bool ok = true;
+            int j = 0;
+            for (int u = u0; u < g.units && ok; u += ustep) {
+                const int row = u / g.n_tiles * nt + row0;
+                for (int c = 2 * k0; c < 2 * k1; ++c, ++j) {
+                    const int s = j % C::AS;
+                    if (!mbar_wait(cv_empty(s), ((j / C::AS) & 1) ^ 1, abort_flag, err)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(tok_full(s), bytes);
+                        tma_load_2d(sbase + C::OFF_B + s * C::B_ITEM, &t_map, c * kItemK, row, tok_full(s), pol);
+                    }
+                    __syncwarp();
+                }
+            }
+            issued = j;
         } else if (warp == 1 && (C::CG == 1 || rank == 0)) {
             // ------------------------------------------------------- MMA issuer
             const uint32_t idesc = idesc_f16_f32(kTileM * C::CG, nt);
@@ -426,7 +448,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const int grp = (warp - 4) >> 2, q = warp & 3;
         const int row = q * 32 + lane;
         const uint32_t tlane = static_cast<uint32_t>(q * 32) << 16;
-        const int pieces = rows * 4;  // 16-byte raw pieces of an item's tokens
         const int total = my_units * unit_items;
         bool ok = true;
         int j = grp;
@@ -436,55 +457,32 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 ok = false;
                 break;
             }
-            // 64 codes of one channel -> 32 TMEM columns of this lane
+            // 64 codes of one channel -> 32 TMEM columns of this lane.  Everything is
+            // done before the wait for the TMEM item: what lies between an item's
+            // release and its next use bounds the ring.
             const uint8_t* wrow = smem + C::OFF_W + rs * C::W_RAW + row * 128;
-            uint4 v[4];
+            uint32_t o[32];
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                v[c] = *reinterpret_cast<const uint4*>(wrow + (((h + c) ^ (row & 7)) << 4));
-            if (!mbar_wait(cv_empty(s), ((j / C::AS) & 1) ^ 1, abort_flag, err)) {
-                ok = false;
-                break;
+            for (int c = 0; c < 4; ++c) {
+                const uint4 v = *reinterpret_cast<const uint4*>(wrow + (((h + c) ^ (row & 7)) << 4));
+                codes_to_f16(v.x, o[8 * c], o[8 * c + 1]);
+                codes_to_f16(v.y, o[8 * c + 2], o[8 * c + 3]);
+                codes_to_f16(v.z, o[8 * c + 4], o[8 * c + 5]);
+                codes_to_f16(v.w, o[8 * c + 6], o[8 * c + 7]);
             }
-            tc_fence_after();
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                uint32_t o[16];
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    codes_to_f16(v[2 * p + c].x, o[8 * c], o[8 * c + 1]);
-                    codes_to_f16(v[2 * p + c].y, o[8 * c + 2], o[8 * c + 3]);
-                    codes_to_f16(v[2 * p + c].z, o[8 * c + 4], o[8 * c + 5]);
-                    codes_to_f16(v[2 * p + c].w, o[8 * c + 6], o[8 * c + 7]);
-                }
-                tmem_st_x16(tmem + tlane + s * C::A_COLS + p * 16, o);
-            }
-            // tokens: piece c of row r (16 codes) becomes two 16-byte pieces of the
-            // 128-byte swizzled fp16 row.  Eight lanes take the four pieces of rows r
-            // and r + 4, the second row's in the other order: reads and writes cover
-            // all banks
-            const uint8_t* traw = smem + C::OFF_T + rs * C::T_RAW;
-            uint8_t* tb = smem + C::OFF_B + s * C::B_ITEM;
-#pragma unroll 2
-            for (int i = q * 32 + lane; i < pieces; i += 128) {
-                const int c = i & 3, r = ((i >> 2) & 1) * 4 + ((i >> 3) & 3) + (i >> 5) * 8;
-                const uint4 x = *reinterpret_cast<const uint4*>(traw + r * 128 + (((h + c) ^ (r & 7)) << 4));
-                uint4 a, b;
-                codes_to_f16(x.x, a.x, a.y);
-                codes_to_f16(x.y, a.z, a.w);
-                codes_to_f16(x.z, b.x, b.y);
-                codes_to_f16(x.w, b.z, b.w);
-                uint8_t* dst = tb + r * 128;
-                const int sw = (r >> 2) & 1, p0 = (2 * c) ^ (r & 7) ^ sw;
-                *reinterpret_cast<uint4*>(dst + (p0 << 4)) = sw ? b : a;
-                *reinterpret_cast<uint4*>(dst + ((p0 ^ 1) << 4)) = sw ? a : b;
-            }
-            // reads of the raw stage before the next TMA into it, writes of the
-            // token item before the MMA reads it
+            // the stage may be filled again (reads ordered before the TMA's writes)
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(raw_empty(rs));
+            // (the arrival below also stands for this CTA's tokens of the item)
+            if (!mbar_wait(tok_full(s), (j / C::AS) & 1, abort_flag, err) ||
+                !mbar_wait(cv_empty(s), ((j / C::AS) & 1) ^ 1, abort_flag, err)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            tmem_st_x32(tmem + tlane + s * C::A_COLS, o);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -500,12 +498,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const int q = warp & 3, half = (warp - C::EPI_WARP0) >> 2;
         const uint32_t tlane = static_cast<uint32_t>(q * 32) << 16;
         const int ncol = nt / 2, col0 = half * ncol;  // (nt % 16 == 0: ncol % 8 == 0)
-        if (g.w_ready)
-            pdl_wait();  // (a_scale, residual)
+        pdl_wait();  // (a_scale, residual)
         int pc = 0;
         bool ok = true;
         for (int u = u0; u < g.units && ok; u += ustep) {
             int sum[C::NTMAX / 2];
+            const int n = u % g.n_tiles * (kTileM * C::CG) + (C::CG == 2 ? rank * kTileM : 0) + q * 32 + lane;
+            const int64_t t0 = static_cast<int64_t>(u / g.n_tiles) * nt + col0;
             for (int c0 = 0; c0 < unit_items; c0 += kChain, ++pc) {
                 const int acc = pc & 1;
                 if (!mbar_wait(acc_full(acc), (pc >> 1) & 1, abort_flag, err)) {
@@ -534,35 +533,28 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
             if (!ok)
                 break;
-            const int r = q * 32 + lane;
             if (g.split > 1) {
-                // (this CTA's only unit: its raw stages have all been converted)
+                // (this CTA's only unit: its stages have all been read)
                 int* part = reinterpret_cast<int*>(smem);
 #pragma unroll
                 for (int j = 0; j < C::NTMAX / 2; ++j)
                     if (j < ncol)
-                        part[(col0 + j) * kTileM + r] = sum[j];
+                        part[(col0 + j) * kTileM + q * 32 + lane] = sum[j];
             } else {
-                const int n = u % g.n_tiles * (kTileM * C::CG) + (C::CG == 2 ? rank * kTileM : 0) + r;
-                const int64_t t0 = static_cast<int64_t>(u / g.n_tiles) * nt + col0;
-                if (n < g.p.N) {
-                    const float ws = g.p.w_scale[n];
-#pragma unroll
-                    for (int j = 0; j < C::NTMAX / 2; j += 8)
-                        if (j < ncol && t0 + j < g.p.T)
-                            store_sums<T>(g.p, t0 + j, 8, n, sum + j, ws);
-                }
+                if (n < g.p.N)
+                    store_sums<T, C::NTMAX / 16>(g.p, t0, ncol, n, sum, g.p.w_scale[n]);
             }
         }
     }
 
     tc_fence_before();
     __syncthreads();
-    if (*abort_flag && warp == 0) {
+    if (*abort_flag && (warp == 0 || warp == 3)) {
         // copies issued but never consumed land before the CTA ends
+        const int depth = warp == 0 ? C::RS : C::AS;
         if (lane == 0)
-            for (int i = issued > C::RS ? issued - C::RS : 0; i < issued; ++i)
-                mbar_drain(raw_full(i % C::RS), (i / C::RS) & 1);
+            for (int i = issued > depth ? issued - depth : 0; i < issued; ++i)
+                mbar_drain(warp == 0 ? raw_full(i % C::RS) : tok_full(i % C::AS), (i / depth) & 1);
         __syncwarp();
     }
     if constexpr (C::CG == 2)
@@ -586,7 +578,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             for (int k = 0; k < g.split; ++k)
                 sum += ld_cluster_s32(at, k);
             if (n0 + r < g.p.N && t0 + col < g.p.T)
-                store_sums<T>(g.p, t0 + col, 1, n0 + r, &sum, g.p.w_scale[n0 + r]);
+                store_sum<T>(g.p, t0 + col, n0 + r, sum, g.p.w_scale[n0 + r]);
         }
         cluster_sync_all();  // (the partial sums stay until every CTA has read them)
     }
@@ -609,20 +601,21 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder()
     return f;
 }
 
-// Rows of 8-bit codes: boxes of `rows` rows x 128 codes, 128-byte swizzle, zero
-// past the last row and past code K of a row.
-cudaError_t codes_rows_map(const int8_t* p, int64_t n, int K, int64_t ld, int rows, CUtensorMap* out)
+// Rows of codes of `size` bytes: boxes of `rows` rows x 128 bytes, 128-byte
+// swizzle, zero past the last row and past code K of a row.
+cudaError_t codes_map(const void* p, int size, int64_t n, int K, int64_t ld, int rows, CUtensorMap* out)
 {
     const auto encode = encoder();
     if (!encode)
         return cudaErrorNotSupported;
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(n)};
     // (a single row has no distance: any multiple of 16 will do)
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld >= K ? ld : (K + 15) / 16 * 16)};
-    const cuuint32_t box[2] = {kRawK, static_cast<cuuint32_t>(rows)}, es[2] = {1, 1};
-    return encode(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(p), dims, strides, box, es,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>((ld >= K ? ld : (K + 15) / 16 * 16) * size)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / size), static_cast<cuuint32_t>(rows)}, es[2] = {1, 1};
+    return encode(out, size == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                  const_cast<void*>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? cudaSuccess
                : cudaErrorInvalidValue;
 }
@@ -644,8 +637,8 @@ cudaError_t launch_cfg(Int8Gemm g, int sms, cudaStream_t s)
         attr_set[dev] = true;
     }
     CUtensorMap wm, tm;
-    if ((e = codes_rows_map(g.p.w, g.p.N, g.p.K, g.p.ld_w, kTileM, &wm)) != cudaSuccess ||
-        (e = codes_rows_map(g.p.a, g.p.T, g.p.K, g.p.ld_a, g.nt / C::CG, &tm)) != cudaSuccess)
+    if ((e = codes_map(g.p.w, 1, g.p.N, g.p.K, g.p.ld_w, kTileM, &wm)) != cudaSuccess ||
+        (e = codes_map(g.p.a16, 2, g.p.T, g.p.K, g.p.ld_a, g.nt / C::CG, &tm)) != cudaSuccess)
         return e;
     const int cluster = C::CG * g.split;
     const int most = g.split > 1 ? g.units : sms / C::CG;  // clusters
@@ -665,16 +658,15 @@ cudaError_t launch_cfg(Int8Gemm g, int sms, cudaStream_t s)
     return cudaLaunchKernelEx(&cfg, int8_gemm_kernel<C, T>, wm, tm, g);
 }
 
-using CfgT32 = Int8Cfg<1, 32, 8, 8, 4>;
-using CfgT128 = Int8Cfg<1, 128, 4, 4, 3, 40, 64, 120>;
-using CfgP160 = Int8Cfg<2, 160, 5, 6, 3, 40, 64, 120>;
+using CfgT32 = Int8Cfg<1, 32, 9, 8, 4>;
+using CfgT128 = Int8Cfg<1, 128, 6, 6, 3, 40, 64, 120>;
+using CfgP160 = Int8Cfg<2, 160, 8, 6, 2, 40, 72, 144>;
 
 template <typename T>
-cudaError_t launch_type(const Int8Args& a, int w_ready, int sms, cudaStream_t s)
+cudaError_t launch_type(const Int8Args& a, int sms, cudaStream_t s)
 {
     Int8Gemm g{};
     g.p = a;
-    g.w_ready = w_ready;
     g.split = 1;
     const int64_t t16 = (a.T + 15) / 16 * 16;
     const int KT = (a.K + kRawK - 1) / kRawK;
@@ -709,9 +701,9 @@ cudaError_t launch_type(const Int8Args& a, int w_ready, int sms, cudaStream_t s)
 
 }  // namespace
 
-cudaError_t launch_int8_gemm(const Int8Args& a, int w_ready, int sms, cudaStream_t s)
+cudaError_t launch_int8_gemm(const Int8Args& a, int sms, cudaStream_t s)
 {
-    return with_type(a.type, [&](auto v) { return launch_type<decltype(v)>(a, w_ready, sms, s); });
+    return with_type(a.type, [&](auto v) { return launch_type<decltype(v)>(a, sms, s); });
 }
 
 }  // namespace chord

@@ -1,6 +1,8 @@
 // int8_kernels.cu -- rows quantised to 8-bit integers with a scale each (plain,
 // or of silu(gate) * up), and the 8-bit product on the CUDA cores for few
 // tokens.
+#include <type_traits>
+
 #include "block_kernels.h"
 #include "device.cuh"
 
@@ -15,31 +17,27 @@ constexpr uint32_t kInfBits = 0x7f800000u;
 constexpr uint32_t kTinyBits = (127u - 100u) << 23;
 
 // Eight consecutive elements of a row from element k (fewer at its end, 0 past
-// it).  VEC: the row is 16-byte aligned, k a multiple of 8.
+// it), as loaded.  VEC: the row is 16-byte aligned, k a multiple of 8.
+template <typename T>
+struct Raw8 {
+    uint4 u[sizeof(T) / 2];
+    __device__ __forceinline__ float at(int i) const { return to_f32<T>(reinterpret_cast<const T*>(u)[i]); }
+};
 template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T* row, int k, int K, float (&v)[8])
+__device__ __forceinline__ Raw8<T> load8(const T* row, int k, int K)
 {
+    Raw8<T> v;
     if (VEC && k + 8 <= K) {
-        if constexpr (sizeof(T) == 4) {
-            const float4 a = *reinterpret_cast<const float4*>(row + k);
-            const float4 b = *reinterpret_cast<const float4*>(row + k + 4);
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-            v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-        } else {
-            union {
-                uint4 u;
-                T e[8];
-            } p;
-            p.u = *reinterpret_cast<const uint4*>(row + k);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                v[i] = to_f32<T>(p.e[i]);
-        }
+        for (unsigned i = 0; i < sizeof(T) / 2; ++i)
+            v.u[i] = reinterpret_cast<const uint4*>(row + k)[i];
     } else {
+        T* e = reinterpret_cast<T*>(v.u);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            v[i] = k + i < K ? to_f32<T>(row[k + i]) : 0.f;
+            e[i] = k + i < K ? row[k + i] : from_f32<T>(0.f);
     }
+    return v;
 }
 
 // silu(g) * u.  The hardware exponential and divide are within a few ulp, far
@@ -49,28 +47,61 @@ __device__ __forceinline__ float silu_mul(float g, float u)
     return __fdividef(g, 1.0f + __expf(-g)) * u;
 }
 
+// What a thread keeps of eight elements between the two passes over its row: the
+// 16-bit values as loaded, or fp32 values.
 template <typename T, bool VEC, bool SILU>
-__device__ __forceinline__ void load8_value(const T* row, int k, int K, float (&v)[8])
-{
-    load8<T, VEC>(row, k, K, v);
-    if constexpr (SILU) {
-        float u[8];
-        load8<T, VEC>(row + K, k, K, u);
+struct Chunk8 {
+    using E = typename std::conditional<SILU, float, T>::type;
+    Raw8<E> v;
+    __device__ __forceinline__ void load(const T* row, int k, int K)
+    {
+        if constexpr (SILU) {
+            const Raw8<T> g = load8<T, VEC>(row, k, K), u = load8<T, VEC>(row + K, k, K);
+            float* e = reinterpret_cast<float*>(v.u);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = silu_mul(v[i], u[i]);
+            for (int i = 0; i < 8; ++i)
+                e[i] = silu_mul(g.at(i), u.at(i));
+        } else {
+            v = load8<T, VEC>(row, k, K);
+        }
     }
-}
+    // Largest magnitude so far, as bits: of a float, or two 16-bit floats side by
+    // side.  On the bits, NaN > inf > every finite value.
+    __device__ __forceinline__ uint32_t max_bits(uint32_t m) const
+    {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(v.u);
+#pragma unroll
+        for (unsigned i = 0; i < 2 * sizeof(E); ++i)
+            m = sizeof(E) == 4 ? max(m, w[i] & 0x7fffffffu) : __vmaxu2(m, w[i] & 0x7fff7fffu);
+        return m;
+    }
+    // ... as the bits of one float
+    static __device__ __forceinline__ uint32_t as_f32_bits(uint32_t m)
+    {
+        if constexpr (sizeof(E) == 4) {
+            return m;
+        } else {
+            const uint16_t h = static_cast<uint16_t>(max(m & 0xffffu, m >> 16));
+            return __float_as_uint(to_f32<E>(*reinterpret_cast<const E*>(&h))) & 0x7fffffffu;
+        }
+    }
+};
+
+// rint(p) + 1.5 * 2^23 for |p| <= 127: the low byte of its bits is the code (ties
+// to even, as the addition rounds)
+constexpr float kRint = 12582912.0f;
 
 // One block per row: the largest magnitude m, then q = rint(x * (127 * (1 / m)))
-// and scale = m / 127.  A thread holds up to NC chunks of 8 elements in registers,
+// and scale = m / 127.  A thread keeps up to NC chunks of 8 elements in registers,
 // so that rows of up to 8 * NC * threads elements are read once; what lies
-// beyond is read again.  m is taken on the bit patterns, where NaN > inf > every
-// finite value: such a row gets codes 0 and the scale NaN, which its products
-// carry on.
+// beyond is read again.  A row with an inf or a NaN gets codes 0 and the scale
+// NaN, which its products carry on.  Bound by its bytes: 16-bit values stay
+// packed for the maximum (two a step), and the codes are rounded by an addition
+// instead of a conversion (16 a clock and SM).
 template <typename T, bool VEC, bool SILU, int NC>
 __global__ void __launch_bounds__(1024) int8_quantize_kernel(QuantArgs a)
 {
+    using C = Chunk8<T, VEC, SILU>;
     __shared__ uint32_t part[32];
     pdl_wait();
     pdl_launch_dependents();
@@ -79,26 +110,24 @@ __global__ void __launch_bounds__(1024) int8_quantize_kernel(QuantArgs a)
     const int nt = blockDim.x, tid = threadIdx.x;
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
         const T* row = static_cast<const T*>(a.x) + t * a.ld_x;
-        float v[NC][8];
+        C v[NC];
         uint32_t m = 0u;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             const int k = 8 * (tid + c * nt);
-            if (k < a.K) {
-                load8_value<T, VEC, SILU>(row, k, a.K, v[c]);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    m = max(m, __float_as_uint(v[c][i]) & 0x7fffffffu);
-            }
+            if (k < a.K)
+                v[c].load(row, k, a.K);
         }
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+            if (8 * (tid + c * nt) < a.K)
+                m = v[c].max_bits(m);
         for (int k = 8 * (tid + NC * nt); k < a.K; k += 8 * nt) {
-            float u[8];
-            load8_value<T, VEC, SILU>(row, k, a.K, u);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                m = max(m, __float_as_uint(u[i]) & 0x7fffffffu);
+            C u;
+            u.load(row, k, a.K);
+            m = u.max_bits(m);
         }
-        m = __reduce_max_sync(kFull, m);
+        m = __reduce_max_sync(kFull, C::as_f32_bits(m));
         if ((tid & 31) == 0)
             part[tid >> 5] = m;
         __syncthreads();
@@ -115,18 +144,36 @@ __global__ void __launch_bounds__(1024) int8_quantize_kernel(QuantArgs a)
         if (tid == 0)
             a.scale[t] = scale;
         int8_t* q = a.q + t * a.ld_q;
-        auto store8 = [&](int k, const float (&x)[8]) {
-            uint32_t w[2] = {0u, 0u};
-            if (inv != 0.f) {
+        __half* q16 = a.q16 + t * a.ld_q;
+        auto store8 = [&](int k, const C& x) {
+            float r[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    w[i >> 2] |= (static_cast<uint32_t>(__float2int_rn(x[i] * inv)) & 0xffu) << (8 * (i & 3));
+            for (int i = 0; i < 8; ++i)
+                r[i] = inv != 0.f ? __fadd_rn(__fmul_rn(x.v.at(i), inv), kRint) : kRint;
+            if (a.q16) {
+                __half2 h[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    h[i] = __floats2half2_rn(r[2 * i] - kRint, r[2 * i + 1] - kRint);
+                if (k + 8 <= a.K) {
+                    *reinterpret_cast<uint4*>(q16 + k) = *reinterpret_cast<const uint4*>(h);
+                } else {
+                    for (int i = 0; k + i < a.K; ++i)
+                        q16[k + i] = __float2half_rn(r[i] - kRint);
+                }
+                return;
             }
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                w[i] = __float_as_uint(r[i]);
             if (k + 8 <= a.K) {
-                *reinterpret_cast<uint2*>(q + k) = make_uint2(w[0], w[1]);
+                *reinterpret_cast<uint2*>(q + k) =
+                    make_uint2(__byte_perm(__byte_perm(w[0], w[1], 0x40), __byte_perm(w[2], w[3], 0x40), 0x5410),
+                               __byte_perm(__byte_perm(w[4], w[5], 0x40), __byte_perm(w[6], w[7], 0x40), 0x5410));
             } else {
                 for (int i = 0; k + i < a.K; ++i)
-                    q[k + i] = static_cast<int8_t>(w[i >> 2] >> (8 * (i & 3)));
+                    q[k + i] = static_cast<int8_t>(w[i]);
             }
         };
 #pragma unroll
@@ -136,10 +183,44 @@ __global__ void __launch_bounds__(1024) int8_quantize_kernel(QuantArgs a)
                 store8(k, v[c]);
         }
         for (int k = 8 * (tid + NC * nt); k < a.K; k += 8 * nt) {
-            float u[8];
-            load8_value<T, VEC, SILU>(row, k, a.K, u);
+            C u;
+            u.load(row, k, a.K);
             store8(k, u);
         }
+    }
+}
+
+// 16 codes per thread
+__global__ void __launch_bounds__(256)
+    int8_to_f16_kernel(const int8_t* a, int64_t ld_a, int64_t T, int K, __half* out, int64_t ld_out, int* err)
+{
+    pdl_wait();
+    pdl_launch_dependents();
+    if (blockIdx.x == 0 && threadIdx.x == 0)
+        *err = 0;
+    const int pieces = (K + 15) / 16;
+    const int64_t total = T * pieces, step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total; i += step) {
+        const int64_t t = i / pieces;
+        const int k = static_cast<int>(i - t * pieces) * 16;
+        __half h[16];
+        if (k + 16 <= K) {
+            union {
+                uint4 u;
+                int8_t c[16];
+            } v;
+            v.u = *reinterpret_cast<const uint4*>(a + t * ld_a + k);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                h[j] = __short2half_rn(v.c[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                h[j] = k + j < K ? __short2half_rn(a[t * ld_a + k + j]) : __half(0.f);
+        }
+        uint4* dst = reinterpret_cast<uint4*>(out + t * ld_out + k);
+        dst[0] = reinterpret_cast<const uint4*>(h)[0];
+        dst[1] = reinterpret_cast<const uint4*>(h)[1];
     }
 }
 
@@ -182,7 +263,7 @@ __global__ void __launch_bounds__(256) int8_rows_kernel(Int8Args a, int ks)
     __shared__ int part[8][kRowsN * TT];
     pdl_launch_dependents();
     pdl_wait();
-    if (a.err && a.clear_err && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0)
+    if (a.err && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0)
         *a.err = 0;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int groups = 8 / ks;
@@ -263,7 +344,6 @@ cudaError_t launch_rows_type(const Int8Args& a, int sms, cudaStream_t s)
         b.out = static_cast<T*>(a.out) + y * tt * a.ld_out;
         if (a.residual)
             b.residual = static_cast<const T*>(a.residual) + y * tt * a.ld_r;
-        b.clear_err = a.clear_err && y == 0;
         const dim3 grid((a.N + per_block - 1) / per_block, static_cast<unsigned>((b.T + tt - 1) / tt));
         cudaError_t e;
         switch (tt) {
@@ -285,15 +365,17 @@ cudaError_t launch_quantize_type(const QuantArgs& a, int sms, cudaStream_t s)
     bool vec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && row_bytes % 16 == 0;
     if (SILU)  // (the up half starts K elements into the row)
         vec = vec && a.K * static_cast<int64_t>(sizeof(T)) % 16 == 0;
+    // chunks a thread keeps: 8 of 16-bit values, 4 of fp32 ones (32 registers)
+    constexpr int NC = sizeof(T) == 2 && !SILU ? 8 : 4;
     const int chunks = (a.K + 7) / 8;
-    // few rows: a chunk per thread, for latency; many: up to four
-    int threads = a.T <= 2 * static_cast<int64_t>(sms) ? chunks : (chunks + 3) / 4;
+    // few rows: a chunk per thread, for latency; many: as many as it keeps
+    int threads = a.T <= 2 * static_cast<int64_t>(sms) ? chunks : (chunks + NC - 1) / NC;
     threads = (threads + 31) / 32 * 32;
     threads = threads < 64 ? 64 : threads > 1024 ? 1024 : threads;
     const int grid = static_cast<int>(a.T < (1 << 30) ? a.T : (1 << 30));
     if (vec)
-        return launch_pdl(int8_quantize_kernel<T, true, SILU, 4>, grid, threads, 0, s, a);
-    return launch_pdl(int8_quantize_kernel<T, false, SILU, 4>, grid, threads, 0, s, a);
+        return launch_pdl(int8_quantize_kernel<T, true, SILU, NC>, grid, threads, 0, s, a);
+    return launch_pdl(int8_quantize_kernel<T, false, SILU, NC>, grid, threads, 0, s, a);
 }
 
 }  // namespace
@@ -304,6 +386,14 @@ cudaError_t launch_int8_quantize(const QuantArgs& a, int sms, cudaStream_t s)
         return a.silu_mul ? launch_quantize_type<decltype(v), true>(a, sms, s)
                           : launch_quantize_type<decltype(v), false>(a, sms, s);
     });
+}
+
+cudaError_t launch_int8_to_f16(const int8_t* a, int64_t ld_a, int64_t T, int K, __half* out, int64_t ld_out,
+                               int* err, int sms, cudaStream_t s)
+{
+    const int64_t blocks = (T * ((K + 15) / 16) + 255) / 256, most = 8 * static_cast<int64_t>(sms);
+    return launch_pdl(int8_to_f16_kernel, static_cast<int>(blocks < most ? blocks : most), 256, 0, s, a, ld_a, T, K,
+                      out, ld_out, err);
 }
 
 cudaError_t launch_int8_rows(const Int8Args& a, int sms, cudaStream_t s)
