@@ -27,6 +27,26 @@ _I32 = (torch.int32,)
 _I8 = (torch.int8,)
 
 
+class _Lib:
+    """The library's functions, bound at the first call (a call's host time counts for one token)."""
+
+    def __getattr__(self, name):
+        fn = getattr(ops.lib(), name)
+        setattr(self, name, fn)
+        return fn
+
+
+_C = _Lib()
+
+
+def _ptr(t) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def _stream(dev) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
 def _rows(t, name: str, dtypes, dev=None, shape=None) -> int:
     """Checks a 2-d tensor of rows with contiguous elements; -> the distance of its rows."""
     if not isinstance(t, torch.Tensor):
@@ -100,10 +120,10 @@ def moe_route(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = None,
     else:
         ids, weights = out
         _pairs(ids, weights, dev, T, k)
-    st = ops.lib().chord_moe_route(ops._p(logits), _TYPES[logits.dtype], T, E, ld, k,
-                                   _SCORES[scoring], ops._p(bias), n_group, topk_group, group_top,
-                                   1 if renormalize else 0, scale, ops._p(ids), ops._p(weights),
-                                   ops._stream(dev))
+    st = _C.chord_moe_route(_ptr(logits), _TYPES[logits.dtype], T, E, ld, k,
+                                   _SCORES[scoring], _ptr(bias), n_group, topk_group, group_top,
+                                   1 if renormalize else 0, scale, _ptr(ids), _ptr(weights),
+                                   _stream(dev))
     B.check(st, "chord_moe_route")
     return ids, weights
 
@@ -136,10 +156,10 @@ def moe_route_backward(d_weights: torch.Tensor, logits: torch.Tensor, topk_ids: 
         ops._req(out, "out", (logits.dtype,), dev, 2)
         if tuple(out.shape) != (T, E):
             raise ValueError(f"out must be [{T}, {E}]")
-    st = ops.lib().chord_moe_route_backward(ops._p(d_weights), ops._p(logits), _TYPES[logits.dtype],
+    st = _C.chord_moe_route_backward(_ptr(d_weights), _ptr(logits), _TYPES[logits.dtype],
                                             T, E, ld, k, _SCORES[scoring], 1 if renormalize else 0,
-                                            scale, ops._p(topk_ids), ops._p(topk_weights),
-                                            ops._p(out), ops._stream(dev))
+                                            scale, _ptr(topk_ids), _ptr(topk_weights),
+                                            _ptr(out), _stream(dev))
     B.check(st, "chord_moe_route_backward")
     return out
 
@@ -162,8 +182,8 @@ def _quantize(x, K: int, ld: int, out, fn: str):
         q, scale = out
         _vec(scale, "scale", dev, T)
     ld_q = _codes(q, "codes", dev, (T, K))
-    st = getattr(ops.lib(), fn)(ops._p(x), _TYPES[x.dtype], T, K, ld, ops._p(q), ld_q,
-                                ops._p(scale), ops._stream(dev))
+    st = getattr(_C, fn)(_ptr(x), _TYPES[x.dtype], T, K, ld, _ptr(q), ld_q,
+                                _ptr(scale), _stream(dev))
     B.check(st, fn)
     return q, scale
 
@@ -211,18 +231,18 @@ def int8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale
     _vec(w_scale, "w_scale", dev, N)
     ld_r = _residual(residual, dev, out_dtype, (T, N))
     out, ld_out = _output(out, dev, out_dtype, (T, N))
-    ws = _workspace(workspace, dev, ops.lib().chord_int8_matmul_workspace_size(T, K))
-    st = ops.lib().chord_int8_matmul(ops._p(a), ld_a, ops._p(a_scale), ops._p(w), ld_w,
-                                     ops._p(w_scale), T, N, K, ops._p(residual), ld_r, ops._p(out),
-                                     _TYPES[out_dtype], ld_out, ops._p(ws), ws.numel(), flags,
-                                     ops._stream(dev))
+    ws = _workspace(workspace, dev, _C.chord_int8_matmul_workspace_size(T, K))
+    st = _C.chord_int8_matmul(_ptr(a), ld_a, _ptr(a_scale), _ptr(w), ld_w,
+                                     _ptr(w_scale), T, N, K, _ptr(residual), ld_r, _ptr(out),
+                                     _TYPES[out_dtype], ld_out, _ptr(ws), ws.numel(), flags,
+                                     _stream(dev))
     B.check(st, "chord_int8_matmul")
     return out
 
 
 def int8_workspace_size(T: int, K: int, I: int = 0) -> int:
     """Workspace bytes of int8_linear (T, K) and of int8_mlp (T, H, I)."""
-    return int(ops.lib().chord_int8_workspace_size(T, K, I))
+    return int(_C.chord_int8_workspace_size(T, K, I))
 
 
 def int8_linear(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
@@ -240,9 +260,9 @@ def int8_linear(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
     ld_r = _residual(residual, dev, x.dtype, (T, N))
     out, ld_out = _output(out, dev, x.dtype, (T, N))
     ws = _workspace(workspace, dev, int8_workspace_size(T, K))
-    st = ops.lib().chord_int8_linear(ops._p(x), _TYPES[x.dtype], ld_x, ops._p(w), ld_w,
-                                     ops._p(w_scale), T, N, K, ops._p(residual), ld_r, ops._p(out),
-                                     ld_out, ops._p(ws), ws.numel(), flags, ops._stream(dev))
+    st = _C.chord_int8_linear(_ptr(x), _TYPES[x.dtype], ld_x, _ptr(w), ld_w,
+                                     _ptr(w_scale), T, N, K, _ptr(residual), ld_r, _ptr(out),
+                                     ld_out, _ptr(ws), ws.numel(), flags, _stream(dev))
     B.check(st, "chord_int8_linear")
     return out
 
@@ -268,10 +288,10 @@ def int8_mlp(x: torch.Tensor, w13: torch.Tensor, w13_scale: torch.Tensor, w2: to
     ld_r = _residual(residual, dev, x.dtype, (T, H))
     out, ld_out = _output(out, dev, x.dtype, (T, H))
     ws = _workspace(workspace, dev, int8_workspace_size(T, H, I))
-    st = ops.lib().chord_int8_mlp(ops._p(x), _TYPES[x.dtype], ld_x, ops._p(w13), ld13,
-                                  ops._p(w13_scale), ops._p(w2), ld2, ops._p(w2_scale), T, H, I,
-                                  ops._p(residual), ld_r, ops._p(out), ld_out, ops._p(ws),
-                                  ws.numel(), flags, ops._stream(dev))
+    st = _C.chord_int8_mlp(_ptr(x), _TYPES[x.dtype], ld_x, _ptr(w13), ld13,
+                                  _ptr(w13_scale), _ptr(w2), ld2, _ptr(w2_scale), T, H, I,
+                                  _ptr(residual), ld_r, _ptr(out), ld_out, _ptr(ws),
+                                  ws.numel(), flags, _stream(dev))
     B.check(st, "chord_int8_mlp")
     return out
 

@@ -17,7 +17,8 @@
 // for all channel tiles: converting them here as well took a third of the
 // converters' time (8192 x 7168 x 4096: 396 us against %TOK).  CG = 2: two CTAs
 // of a cluster share a tile (cta_group::2); each holds 128 channels and half of
-// the tokens.  A raw stage is 128 codes deep, an item 64 of them.
+// the tokens.  A raw stage is 128 codes deep, an item (what the
+// issuer waits for and releases at once) 64 or 128.
 //   warp 0       weight producer: a TMA box per raw stage
 //   warp 1       MMA issuer (of the first CTA);  warp 2  owner of tensor memory
 //   warp 3       token producer: a TMA box per item
@@ -42,8 +43,8 @@ namespace chord {
 namespace {
 
 constexpr int kRawK = 128;   // codes of a raw stage (one 128-byte swizzled row)
-constexpr int kItemK = 64;   // codes of an item (one 128-byte swizzled fp16 row)
-constexpr int kChain = 16;   // items of an accumulation chain (1024 products)
+constexpr int kHalfK = 64;   // codes a converter group takes at a time (128 bytes as fp16)
+constexpr int kChainK = 1024;  // products of an accumulation chain
 constexpr int kTileM = 128;  // channels of a CTA's tile
 constexpr int kEpiWarps = 8;
 
@@ -55,36 +56,41 @@ struct Int8Gemm {
     int split;     // CTAs of a cluster that share a unit along K (CG = 1)
 };
 
-// CG CTAs per tile, token tile, raw weight stages, items in flight (weights in
-// tensor memory, tokens in shared memory: one ring), converter groups, and the
-// registers of a producer / converter / epilogue thread (0: as launched)
-template <int CG_, int NTMAX_, int RS_, int AS_, int NG_, int R0_ = 0, int RC_ = 0, int RE_ = 0>
+// CG CTAs per tile, token tile, raw weight stages, halves of 64 codes per item,
+// items in flight (weights in tensor memory, tokens in shared memory: one ring),
+// converter groups, and the registers of a producer / converter / epilogue
+// thread (0: as launched)
+template <int CG_, int NTMAX_, int RS_, int HV_, int AS_, int NG_, int R0_ = 0, int RC_ = 0, int RE_ = 0>
 struct Int8Cfg {
     static constexpr int CG = CG_;
     static constexpr int NTMAX = NTMAX_;
     static constexpr int RS = RS_;
+    static constexpr int HV = HV_;
     static constexpr int AS = AS_;
+    static constexpr int CHAIN = kChainK / (kHalfK * HV);  // items of a chain
     static constexpr int NG = NG_;
     static constexpr int R0 = R0_, RC = RC_, RE = RE_;
     static constexpr int EPI_WARP0 = 4 + 4 * NG;
     static constexpr int THREADS = 32 * (EPI_WARP0 + kEpiWarps);
     static constexpr int ROWS = NTMAX / CG;  // token rows of a CTA
     static constexpr int W_RAW = kTileM * kRawK;
-    static constexpr int B_ITEM = ROWS * 128;
+    static constexpr int B_HALF = ROWS * 128;  // tokens of 64 codes
+    static constexpr int B_ITEM = HV * B_HALF;
     static constexpr int OFF_W = 0;
     static constexpr int OFF_B = OFF_W + RS * W_RAW;
     static constexpr int OFF_BARS = OFF_B + AS * B_ITEM;
     static constexpr int NBARS = 2 * RS + 3 * AS + 4 + 1;
     static constexpr int OFF_MISC = OFF_BARS + 8 * NBARS;
     static constexpr int SMEM = OFF_MISC + 16 + 1024;  // + alignment slack
-    static constexpr int A_COLS = kItemK / 2;
+    static constexpr int A_COLS = HV * kHalfK / 2;
     static constexpr int D_COL0 = AS * A_COLS;
     static constexpr int TMEM_COLS = 512;
     static_assert(NTMAX % (16 * CG) == 0 && NTMAX <= 256, "token tile");
-    static_assert(B_ITEM % 1024 == 0, "swizzle atoms need 1024-byte alignment");
+    static_assert(B_HALF % 1024 == 0, "swizzle atoms need 1024-byte alignment");
     static_assert(D_COL0 + 2 * NTMAX <= TMEM_COLS, "tensor memory budget");
     static_assert(SMEM <= 232448 && SMEM > 116 * 1024, "one CTA per SM");
-    static_assert(NG <= AS && NG <= 2 * RS, "a group never waits for an item of its own");
+    static_assert(HV == 1 || HV == 2, "halves");
+    static_assert(NG <= HV * AS && NG <= 2 * RS, "a group never waits for an item of its own");
     // what the warpgroups take may not exceed what the CTA was launched with
     static constexpr int REGS = 65536 / THREADS / 8 * 8;
     static_assert(R0 + NG * RC + 2 * RE <= (3 + NG) * REGS, "register shares");
@@ -152,33 +158,43 @@ __device__ __forceinline__ void tmem_dealloc_cg(uint32_t taddr, uint32_t ncols)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
-// An item's four K = 16 MMAs from one elected lane of a converged warp: A columns
-// a + 8 j, B 32-byte step j of the swizzled row.  accumulate = 0: the first
-// overwrites D.
-#define CHORD_INT8_MMA4(GROUP)                                                                            \
+// The K = 16 MMAs of an item (four for each half of 64 codes) from one elected
+// lane of a converged warp: A columns a + 8 j, B 32-byte step j % 4 of the swizzled
+// row in column block j / 4 (HALF16: a block's size in 16-byte units).
+// accumulate = 0: the first overwrites D.
+#define CHORD_INT8_MMA4(GROUP, P0)                                                                        \
+    "mov.b64 bd, {bq, %3};\n\t@e tcgen05.mma." GROUP ".kind::f16 [%0], [aq], bd, %4, " P0 ";\n\t"         \
+    "add.u32 bl, bq, 2;\n\tmov.b64 bd, {bl, %3};\n\tadd.u32 al, aq, 8;\n\t"                               \
+    "@e tcgen05.mma." GROUP ".kind::f16 [%0], [al], bd, %4, pt;\n\t"                                      \
+    "add.u32 bl, bq, 4;\n\tmov.b64 bd, {bl, %3};\n\tadd.u32 al, aq, 16;\n\t"                              \
+    "@e tcgen05.mma." GROUP ".kind::f16 [%0], [al], bd, %4, pt;\n\t"                                      \
+    "add.u32 bl, bq, 6;\n\tmov.b64 bd, {bl, %3};\n\tadd.u32 al, aq, 24;\n\t"                              \
+    "@e tcgen05.mma." GROUP ".kind::f16 [%0], [al], bd, %4, pt;\n\t"
+#define CHORD_INT8_ITEM(GROUP, SECOND)                                                                    \
     asm volatile(                                                                                         \
-        "{\n\t.reg .pred e, p0, pt;\n\t.reg .b32 bl, al;\n\t.reg .b64 bd;\n\t"                            \
+        "{\n\t.reg .pred e, p0, pt;\n\t.reg .b32 bq, bl, aq, al;\n\t.reg .b64 bd;\n\t"                    \
         "setp.ne.b32 p0, %5, 0;\n\tsetp.eq.b32 pt, 0, 0;\n\telect.sync _|e, 0xffffffff;\n\t"              \
-        "mov.b64 bd, {%2, %3};\n\t@e tcgen05.mma." GROUP ".kind::f16 [%0], [%1], bd, %4, p0;\n\t"         \
-        "add.u32 bl, %2, 2;\n\tmov.b64 bd, {bl, %3};\n\tadd.u32 al, %1, 8;\n\t"                            \
-        "@e tcgen05.mma." GROUP ".kind::f16 [%0], [al], bd, %4, pt;\n\t"                                  \
-        "add.u32 bl, %2, 4;\n\tmov.b64 bd, {bl, %3};\n\tadd.u32 al, %1, 16;\n\t"                           \
-        "@e tcgen05.mma." GROUP ".kind::f16 [%0], [al], bd, %4, pt;\n\t"                                  \
-        "add.u32 bl, %2, 6;\n\tmov.b64 bd, {bl, %3};\n\tadd.u32 al, %1, 24;\n\t"                           \
-        "@e tcgen05.mma." GROUP ".kind::f16 [%0], [al], bd, %4, pt;\n\t}" ::"r"(d),                       \
+        "mov.b32 bq, %2;\n\tmov.b32 aq, %1;\n\t" CHORD_INT8_MMA4(GROUP, "p0") SECOND "}" ::"r"(d),        \
         "r"(a), "r"(static_cast<uint32_t>(b_desc)), "r"(static_cast<uint32_t>(b_desc >> 32)), "r"(idesc), \
-        "r"(accumulate)                                                                                   \
+        "r"(accumulate), "n"(HALF16)                                                                      \
         : "memory")
-template <int CG>
+#define CHORD_INT8_SECOND(GROUP) "add.u32 bq, bq, %6;\n\tadd.u32 aq, aq, 32;\n\t" CHORD_INT8_MMA4(GROUP, "pt")
+template <int CG, int HV, int HALF16>
 __device__ __forceinline__ void mma_item(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc,
                                          uint32_t accumulate)
 {
-    if constexpr (CG == 1)
-        CHORD_INT8_MMA4("cta_group::1");
+    if constexpr (CG == 1 && HV == 1)
+        CHORD_INT8_ITEM("cta_group::1", "");
+    else if constexpr (CG == 1)
+        CHORD_INT8_ITEM("cta_group::1", CHORD_INT8_SECOND("cta_group::1"));
+    else if constexpr (HV == 1)
+        CHORD_INT8_ITEM("cta_group::2", "");
     else
-        CHORD_INT8_MMA4("cta_group::2");
+        CHORD_INT8_ITEM("cta_group::2", CHORD_INT8_SECOND("cta_group::2"));
 }
 #undef CHORD_INT8_MMA4
+#undef CHORD_INT8_ITEM
+#undef CHORD_INT8_SECOND
 
 // Arrives on `bar` (of both CTAs of a pair) when the MMAs issued so far are done.
 template <int CG>
@@ -318,11 +334,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::RS; ++s) {
             mbar_init(raw_full(s), 1);
-            mbar_init(raw_empty(s), 8);  // (the four warps of the groups of its two items)
+            mbar_init(raw_empty(s), 8);  // (four warps for each half)
         }
         for (int s = 0; s < C::AS; ++s) {
             mbar_init(tok_full(s), 1);
-            mbar_init(cv_full(s), 4 * C::CG);
+            mbar_init(cv_full(s), 4 * C::HV * C::CG);
             mbar_init(cv_empty(s), 1);
         }
         for (int s = 0; s < 2; ++s) {
@@ -351,7 +367,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     const int k0 = krank * KT / g.split, k1 = (krank + 1) * KT / g.split;
     const int u0 = blockIdx.x / cluster, ustep = gridDim.x / cluster;
     const int my_units = u0 < g.units ? (g.units - 1 - u0) / ustep + 1 : 0;
-    const int unit_items = 2 * (k1 - k0);
+    const int unit_items = (k1 - k0) * (2 / C::HV);
     const int nt = g.nt;
     const int rows = nt / C::CG;
     int issued = 0;  // weight / token producer: stages whose copies were issued
@@ -384,13 +400,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             // --------------------------------------------------- token producer
             pdl_wait();  // (the weights are under way while the tokens are still written)
             const uint64_t pol = policy_evict_last();
-            const uint32_t bytes = rows * 128;
+            const uint32_t bytes = C::HV * rows * 128;
             const int row0 = C::CG == 2 ? rank * rows : 0;
             bool ok = true;
             int j = 0;
             for (int u = u0; u < g.units && ok; u += ustep) {
                 const int row = u / g.n_tiles * nt + row0;
-                for (int c = 2 * k0; c < 2 * k1; ++c, ++j) {
+                int k = k0 * kRawK;
+                for (int c = 0; c < unit_items; ++c, ++j) {
                     const int s = j % C::AS;
                     if (!mbar_wait(cv_empty(s), ((j / C::AS) & 1) ^ 1, abort_flag, err)) {
                         ok = false;
@@ -398,8 +415,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     }
                     if (lane == 0) {
                         mbar_arrive_expect_tx(tok_full(s), bytes);
-                        tma_load_2d(sbase + C::OFF_B + s * C::B_ITEM, &t_map, c * kItemK, row, tok_full(s), pol);
+                        const uint32_t dst = sbase + C::OFF_B + s * C::B_ITEM;
+#pragma unroll
+                        for (int h = 0; h < C::HV; ++h)
+                            tma_load_2d(dst + h * C::B_HALF, &t_map, k + h * kHalfK, row, tok_full(s), pol);
                     }
+                    k += C::HV * kHalfK;
                     __syncwarp();
                 }
             }
@@ -407,30 +428,34 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         } else if (warp == 1 && (C::CG == 1 || rank == 0)) {
             // ------------------------------------------------------- MMA issuer
             const uint32_t idesc = idesc_f16_f32(kTileM * C::CG, nt);
-            int j = 0, pc = 0, any = 0;
+            const uint64_t bdesc0 = smem_desc_sw128(sbase + C::OFF_B);
+            int s = 0, pc = 0, any = 0;
+            uint32_t phase = 0;
             bool ok = true;
             for (int u = 0; u < my_units && ok; ++u) {
-                for (int c0 = 0; c0 < unit_items && ok; c0 += kChain, ++pc) {
-                    const int c1 = c0 + kChain < unit_items ? c0 + kChain : unit_items;
+                for (int c0 = 0; c0 < unit_items && ok; c0 += C::CHAIN, ++pc) {
+                    const int c1 = c0 + C::CHAIN < unit_items ? c0 + C::CHAIN : unit_items;
                     const int acc = pc & 1;
-                    if (!__all_sync(0xffffffffu, mbar_wait(acc_empty(acc), ((pc >> 1) & 1) ^ 1,
-                                                                   abort_flag, err))) {
+                    const uint32_t d = tmem + C::D_COL0 + acc * C::NTMAX;
+                    if (!__all_sync(0xffffffffu,
+                                    mbar_wait(acc_empty(acc), ((pc >> 1) & 1) ^ 1, abort_flag, err))) {
                         ok = false;
                         break;
                     }
-                    for (int c = c0; c < c1; ++c, ++j) {
-                        const int s = j % C::AS;
-                        if (!__all_sync(0xffffffffu,
-                                        mbar_wait(cv_full(s), (j / C::AS) & 1, abort_flag, err))) {
+                    for (int c = c0; c < c1; ++c) {
+                        if (!__all_sync(0xffffffffu, mbar_wait(cv_full(s), phase, abort_flag, err))) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
-                        mma_item<C::CG>(tmem + C::D_COL0 + acc * C::NTMAX, tmem + s * C::A_COLS,
-                                        smem_desc_sw128(sbase + C::OFF_B + s * C::B_ITEM), idesc,
-                                        c != c0 ? 1u : 0u);
+                        mma_item<C::CG, C::HV, C::B_HALF / 16>(d, tmem + s * C::A_COLS, bdesc0 + s * (C::B_ITEM / 16),
+                                                        idesc, c != c0 ? 1u : 0u);
                         any = 1;
                         commit_elect<C::CG>(cv_empty(s));
+                        if (++s == C::AS) {
+                            s = 0;
+                            phase ^= 1u;
+                        }
                     }
                     if (ok)
                         commit_elect<C::CG>(acc_full(acc));
@@ -448,12 +473,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const int grp = (warp - 4) >> 2, q = warp & 3;
         const int row = q * 32 + lane;
         const uint32_t tlane = static_cast<uint32_t>(q * 32) << 16;
-        const int total = my_units * unit_items;
+        const int total = C::HV * my_units * unit_items;  // halves
         bool ok = true;
         int j = grp;
         for (; j < total; j += C::NG) {
-            const int rs = (j >> 1) % C::RS, s = j % C::AS, h = (j & 1) * 4;
-            if (!mbar_wait(raw_full(rs), ((j >> 1) / C::RS) & 1, abort_flag, err)) {
+            const int st = j >> 1, h = j & 1, rs = st % C::RS;  // raw stage, its half
+            const int it = j / C::HV, s = it % C::AS;            // item
+            if (!mbar_wait(raw_full(rs), (st / C::RS) & 1, abort_flag, err)) {
                 ok = false;
                 break;
             }
@@ -464,7 +490,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             uint32_t o[32];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                const uint4 v = *reinterpret_cast<const uint4*>(wrow + (((h + c) ^ (row & 7)) << 4));
+                const uint4 v = *reinterpret_cast<const uint4*>(wrow + (((4 * h + c) ^ (row & 7)) << 4));
                 codes_to_f16(v.x, o[8 * c], o[8 * c + 1]);
                 codes_to_f16(v.y, o[8 * c + 2], o[8 * c + 3]);
                 codes_to_f16(v.z, o[8 * c + 4], o[8 * c + 5]);
@@ -476,13 +502,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             if (lane == 0)
                 mbar_arrive(raw_empty(rs));
             // (the arrival below also stands for this CTA's tokens of the item)
-            if (!mbar_wait(tok_full(s), (j / C::AS) & 1, abort_flag, err) ||
-                !mbar_wait(cv_empty(s), ((j / C::AS) & 1) ^ 1, abort_flag, err)) {
+            if (!mbar_wait(tok_full(s), (it / C::AS) & 1, abort_flag, err) ||
+                !mbar_wait(cv_empty(s), ((it / C::AS) & 1) ^ 1, abort_flag, err)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            tmem_st_x32(tmem + tlane + s * C::A_COLS, o);
+            tmem_st_x32(tmem + tlane + s * C::A_COLS + (j % C::HV) * (kHalfK / 2), o);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -490,8 +516,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 arrive_first<C::CG>(cv_full(s));
         }
         // (pair: the last arrivals from the first CTA's commits have landed)
-        if (C::CG == 2 && ok && j > grp)
-            mbar_wait(cv_empty((j - C::NG) % C::AS), ((j - C::NG) / C::AS) & 1, abort_flag, err);
+        if (C::CG == 2 && ok && j > grp) {
+            const int it = (j - C::NG) / C::HV;
+            mbar_wait(cv_empty(it % C::AS), (it / C::AS) & 1, abort_flag, err);
+        }
     } else {
         // -------------------------------------------------------------- epilogue
         set_regs_inc<C::RE>();
@@ -505,7 +533,20 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             int sum[C::NTMAX / 2];
             const int n = u % g.n_tiles * (kTileM * C::CG) + (C::CG == 2 ? rank * kTileM : 0) + q * 32 + lane;
             const int64_t t0 = static_cast<int64_t>(u / g.n_tiles) * nt + col0;
-            for (int c0 = 0; c0 < unit_items; c0 += kChain, ++pc) {
+            if (g.p.residual && g.split == 1) {
+                // the tile's residual comes into L2 while the unit is computed, a share
+                // of its 128-byte lines by each warp (rows may start inside a line)
+                constexpr int kLine = 128 / static_cast<int>(sizeof(T)), kLines = kTileM / kLine + 1;
+                const int n0 = n - (q * 32 + lane);
+                for (int i = threadIdx.x - C::EPI_WARP0 * 32; i < nt * kLines; i += kEpiWarps * 32) {
+                    const int64_t t = t0 - col0 + i / kLines;
+                    const int c = n0 + i % kLines * kLine;
+                    if (t < g.p.T && c < g.p.N)
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const T*>(g.p.residual) +
+                                                                      t * g.p.ld_r + c));
+                }
+            }
+            for (int c0 = 0; c0 < unit_items; c0 += C::CHAIN, ++pc) {
                 const int acc = pc & 1;
                 if (!mbar_wait(acc_full(acc), (pc >> 1) & 1, abort_flag, err)) {
                     ok = false;
@@ -658,9 +699,12 @@ cudaError_t launch_cfg(Int8Gemm g, int sms, cudaStream_t s)
     return cudaLaunchKernelEx(&cfg, int8_gemm_kernel<C, T>, wm, tm, g);
 }
 
-using CfgT32 = Int8Cfg<1, 32, 9, 8, 4>;
-using CfgT128 = Int8Cfg<1, 128, 6, 6, 3, 40, 64, 120>;
-using CfgP160 = Int8Cfg<2, 160, 8, 6, 2, 40, 72, 144>;
+// 64-code items: more of them in flight in the same tensor memory, which the
+// round trip between the two CTAs of a pair needs; 128: fewer turns of the issuer,
+// for which a small tile is too short
+using CfgT32 = Int8Cfg<1, 32, 9, 2, 4, 4>;
+using CfgT128 = Int8Cfg<1, 128, 5, 2, 4, 3, 40, 64, 120>;
+using CfgP160 = Int8Cfg<2, 160, 8, 1, 6, 2, 40, 72, 144>;
 
 template <typename T>
 cudaError_t launch_type(const Int8Args& a, int sms, cudaStream_t s)
