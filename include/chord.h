@@ -464,7 +464,8 @@ chord_status chord_moe_route(const void* logits, int type, int64_t T, int E, int
  * the bias and the groups) is a constant.  d_weights, topk_ids and topk_weights
  * are [T, k] (gradient of, and what chord_moe_route returned); scoring,
  * renormalize and scale as there.  d_logits, device [T, E] of `type`, densely
- * packed, is written entirely.  An id outside [0, E) gives no gradient.
+ * packed, is written entirely.  A token's ids are distinct, as chord_moe_route
+ * returns them; one outside [0, E) gives no gradient.
  */
 chord_status chord_moe_route_backward(const float* d_weights, const void* logits, int type,
                                       int64_t T, int E, int64_t ld, int k, int scoring,

@@ -32,11 +32,14 @@ __device__ __forceinline__ float order_value(uint32_t k)
 
 // A logit as the router sees it: NaN and -inf are masked (-inf), +inf counts
 // as the largest finite float, -0 as 0.
+__device__ __forceinline__ float clamp_logit(float v)
+{
+    return v == v ? fminf(v, FLT_MAX) + 0.f : -INFINITY;
+}
 template <typename T>
 __device__ __forceinline__ float load_logit(const T* p)
 {
-    const float v = to_f32<T>(*p);
-    return v == v ? fminf(v, FLT_MAX) + 0.f : -INFINITY;
+    return clamp_logit(to_f32<T>(*p));
 }
 
 __device__ __forceinline__ float warp_max(float v)
@@ -88,108 +91,220 @@ __device__ uint32_t choose_groups(const float* vals, const MoeRouteArgs& a, int 
     return kept;
 }
 
-// One warp routes one token; lane l holds experts l, l + 32, ... (NI of them).
-// k rounds pick the largest key and, among equal keys, the lowest expert: each
-// lane keeps its own best, two warp reductions find the winner, and only then
-// the winner's lane looks for its next best.
-template <typename TL, int NI>
-__device__ void route_token(const MoeRouteArgs& a, int64_t t, int lane, float* vals)
+// Q consecutive elements.
+template <typename T, int Q>
+struct Elems {
+    T v[Q];
+    __device__ __forceinline__ void load(const T* p)
+    {
+        if constexpr (Q * sizeof(T) == 16)
+            *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(p);
+        else if constexpr (Q * sizeof(T) == 8)
+            *reinterpret_cast<uint2*>(v) = *reinterpret_cast<const uint2*>(p);
+        else
+            v[0] = *p;
+    }
+};
+
+// Shared memory of one token: keys [E], with groups values [E], and with several
+// warps their partial results and candidates (2 x 32 words each).
+template <int W>
+__host__ __device__ constexpr int route_words(int E, bool groups)
+{
+    return (E + 3) / 4 * 4 * (groups ? 2 : 1) + (W > 1 ? W * 64 + 2 * W : 0);
+}
+
+// W warps route one token, each its part of the experts; a lane takes Q
+// consecutive ones a turn (Q = 4: rows and bias 16-byte aligned, E a multiple of
+// 4).  The keys go to shared memory.  k rounds pick a warp's largest key and,
+// among equal keys, the lowest expert.  A round is a chain of dependent steps, so
+// it is kept short: each lane has its two best at hand (a third from one lane is
+// rare: 5 % of the tokens at 8 of 384 in one warp), and a round is one warp
+// maximum and a vote.  The warps' choices, W sorted lists, are merged the same
+// way.  What bounds it: few tokens, the latency of one instruction after another
+// in a warp (one token of 384 experts with one warp: 1700 instructions, 8.1 us;
+// four warps: %R1); many, instruction issue (8192 tokens: 1840 instructions a
+// token one element at a time, 19.4 us; now %R2).
+template <typename TL, int W, int Q>
+__device__ void route_token(const MoeRouteArgs& a, int64_t t, int warp, int lane, uint32_t* keys)
 {
     const TL* row = static_cast<const TL*>(a.logits) + t * a.ld;
-    const bool sigmoid = a.scoring == CHORD_SCORE_SIGMOID;
-    float x[NI];
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-        const int e = lane + 32 * i;
-        x[i] = e < a.E ? load_logit(row + e) : -INFINITY;
-    }
+    const bool sigmoid = a.scoring == CHORD_SCORE_SIGMOID, groups = a.n_group > 1;
+    float* vals = reinterpret_cast<float*>(keys + (a.E + 3) / 4 * 4);
+    uint32_t* cand = keys + (a.E + 3) / 4 * 4 * (groups ? 2 : 1);  // [W][32] keys, [W][32] experts
+    float* part = reinterpret_cast<float*>(cand + W * 64);
+    auto sync = [&]() {
+        if constexpr (W > 1)
+            __syncthreads();
+        else
+            __syncwarp();
+    };
+    const int share = (a.E + 4 * W - 1) / (4 * W) * 4;  // experts of a warp
+    const int lo = warp * share, hi = min(lo + share, a.E);
+
     float top = 0.f, sum = 1.f;  // softmax: largest logit, sum of exponentials
-    if (!sigmoid) {
-        float m = x[0];
+    // This lane's two largest keys (ties: the lower expert first); 0: none.
+    uint32_t b1 = 0u, b2 = 0u;
+    int e1 = 0, e2 = 0;
+    auto push = [&](uint32_t k, int e) {
+        const bool first = k > b1, second = k > b2;
+        e2 = first ? e1 : second ? e : e2;
+        b2 = first ? b1 : second ? k : b2;
+        e1 = first ? e : e1;
+        b1 = first ? k : b1;
+    };
+    // keys: score + bias, or without a bias the logits, whose order is that of
+    // the scores; groups are ranked by score + bias (without a bias by the
+    // scores, for softmax before the division by their sum)
+    auto take = [&](const float (&x)[Q], int e) {
+        Elems<float, Q> bias;
+        if (a.bias)
+            bias.load(a.bias + e);
+        Elems<uint32_t, Q> k;
 #pragma unroll
-        for (int i = 1; i < NI; ++i)
-            m = fmaxf(m, x[i]);
-        top = warp_max(m);
+        for (int i = 0; i < Q; ++i) {
+            const bool real = x[i] != -INFINITY;
+            float v = x[i];
+            if (a.bias || groups) {
+                v = sigmoid ? sigmoid_f32(x[i]) : expf(x[i] - top);
+                if (a.bias) {
+                    v = (sigmoid ? v : v / sum) + bias.v[i] + 0.f;
+                    v = v == v ? v : -INFINITY;  // (a NaN bias masks its expert)
+                }
+                if (groups)
+                    vals[e + i] = real ? v : -INFINITY;
+            }
+            k.v[i] = real ? order_key(a.bias ? v : x[i]) : kKeyMasked;
+            if (!groups)
+                push(k.v[i], e + i);
+        }
+        if constexpr (Q == 4)
+            *reinterpret_cast<uint4*>(keys + e) = *reinterpret_cast<const uint4*>(k.v);
+        else
+            keys[e] = k.v[0];
+    };
+    // four turns' loads in flight; softmax only notes the logits and their maximum
+    float m = -INFINITY;
+    for (int e0 = lo + Q * lane; e0 < hi; e0 += 128 * Q) {
+        Elems<TL, Q> raw[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (e0 + 32 * Q * j < hi)
+                raw[j].load(row + e0 + 32 * Q * j);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (e0 + 32 * Q * j < hi) {
+                float x[Q];
+#pragma unroll
+                for (int i = 0; i < Q; ++i) {
+                    x[i] = clamp_logit(to_f32<TL>(raw[j].v[i]));
+                    m = fmaxf(m, x[i]);
+                    if (!sigmoid)
+                        keys[e0 + 32 * Q * j + i] = __float_as_uint(x[i]);
+                }
+                if (sigmoid)
+                    take(x, e0 + 32 * Q * j);
+            }
+    }
+    if (!sigmoid) {
+        // a value of every warp, combined
+        auto across = [&](float v, bool add) {
+            if constexpr (W > 1) {
+                __syncthreads();
+                if (lane == 0)
+                    part[warp] = v;
+                __syncthreads();
+                v = part[0];
+                for (int i = 1; i < W; ++i)
+                    v = add ? v + part[i] : fmaxf(v, part[i]);
+            }
+            return v;
+        };
+        top = across(warp_max(m), false);
         if (top == -INFINITY)
             top = 0.f;  // every expert is masked: every exponential is 0
         if (a.bias || !a.renorm) {
             sum = 0.f;
+            for (int e = lo + Q * lane; e < hi; e += 32 * Q)
 #pragma unroll
-            for (int i = 0; i < NI; ++i)
-                sum += expf(x[i] - top);
-            sum = warp_sum(sum);
+                for (int i = 0; i < Q; ++i)
+                    sum += expf(__uint_as_float(keys[e + i]) - top);
+            sum = across(warp_sum(sum), true);
+        }
+        for (int e = lo + Q * lane; e < hi; e += 32 * Q) {
+            float x[Q];
+#pragma unroll
+            for (int i = 0; i < Q; ++i)
+                x[i] = __uint_as_float(keys[e + i]);
+            take(x, e);
         }
     }
-    // keys: score + bias, or without a bias the logits, whose order is that of
-    // the scores; groups are ranked by score + bias (without a bias by the
-    // scores, for softmax before the division by their sum)
-    uint32_t key[NI];
-    if (a.bias || a.n_group > 1) {
+    if (groups) {
+        const int size = a.E / a.n_group;
+        sync();
+        const uint32_t kept = choose_groups(vals, a, size, lane);
+        // e / size for e < 1024: e * ceil(2^20 / size) >> 20 is exact
+        const uint32_t magic = ((1u << 20) + size - 1) / size;
+        for (int e0 = lo + Q * lane; e0 < hi; e0 += 32 * Q)
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const int e = lane + 32 * i;
-            const bool real = x[i] != -INFINITY;
-            float v = -INFINITY;
-            if (real) {
-                v = sigmoid ? sigmoid_f32(x[i]) : expf(x[i] - top);
-                if (a.bias) {
-                    v = (sigmoid ? v : v / sum) + a.bias[e] + 0.f;
-                    v = v == v ? v : -INFINITY;  // (a NaN bias masks its expert)
-                }
+            for (int i = 0; i < Q; ++i) {
+                const int e = e0 + i;
+                const uint32_t k = (kept >> ((e * magic) >> 20)) & 1u ? keys[e] : kKeyMasked;
+                keys[e] = k;
+                push(k, e);
             }
-            if (e < a.E && a.n_group > 1)
-                vals[e] = v;
-            key[i] = e >= a.E ? 0u : !real ? kKeyMasked : order_key(a.bias ? v : x[i]);
-        }
-        if (a.n_group > 1) {
-            const int size = a.E / a.n_group;
-            __syncwarp();
-            const uint32_t kept = choose_groups(vals, a, size, lane);
-            __syncwarp();
-            // e / size for e < 1024: e * ceil(2^20 / size) >> 20 is exact
-            const uint32_t magic = ((1u << 20) + size - 1) / size;
-#pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                const uint32_t e = lane + 32 * i;
-                if (key[i] != 0u && !((kept >> ((e * magic) >> 20)) & 1u))
-                    key[i] = kKeyMasked;
-            }
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < NI; ++i)
-            key[i] = lane + 32 * i >= a.E ? 0u : order_key(x[i]);
     }
 
-    int my_id = 0;          // lane j keeps the j-th choice
+    int my_id = 0;  // lane j keeps the j-th choice
     uint32_t my_key = 0u;
-    uint32_t best = 0u;     // this lane's largest key and its lowest expert
-    int best_e = 0;
-    auto refresh = [&]() {
-        best = key[0];
-#pragma unroll
-        for (int i = 1; i < NI; ++i)
-            best = max(best, key[i]);
-#pragma unroll
-        for (int i = NI - 1; i >= 0; --i)
-            if (key[i] == best)
-                best_e = lane + 32 * i;
+    auto rounds = [&](auto&& next) {  // next(m, e): the winner's lane moves on from (m, e)
+#pragma unroll 1
+        for (int j = 0; j < a.k; ++j) {
+            const uint32_t m = __reduce_max_sync(kFull, b1);
+            uint32_t tied = __ballot_sync(kFull, b1 == m);
+            if (tied & (tied - 1u)) {  // (several lanes: the lowest expert)
+                const int e = __reduce_min_sync(kFull, b1 == m ? e1 : INT_MAX);
+                tied = __ballot_sync(kFull, b1 == m && e1 == e);
+            }
+            const int w = __ffs(tied) - 1;
+            const int e = __shfl_sync(kFull, e1, w);
+            if (lane == j) {
+                my_id = e;
+                my_key = m;
+            }
+            if (lane == w)
+                next(m, e);
+        }
     };
-    refresh();
-    for (int j = 0; j < a.k; ++j) {
-        const uint32_t m = __reduce_max_sync(kFull, best);
-        const int e = __reduce_min_sync(kFull, best == m ? best_e : INT_MAX);
-        if (lane == j) {
-            my_id = e;
-            my_key = m;
-        }
-        if ((e & 31) == lane) {
+    rounds([&](uint32_t m, int e) {
+        b1 = b2;
+        e1 = e2;
+        b2 = 0u;
+        if (b1 == 0u)  // a third choice of one lane: look again, at what comes after
+            for (int e0 = lo + Q * lane; e0 < hi; e0 += 32 * Q)
 #pragma unroll
-            for (int i = 0; i < NI; ++i)
-                if (lane + 32 * i == e)
-                    key[i] = 0u;
-            refresh();
-        }
+                for (int i = 0; i < Q; ++i) {
+                    const uint32_t k = keys[e0 + i];
+                    push(k < m || (k == m && e0 + i > e) ? k : 0u, e0 + i);
+                }
+    });
+    if constexpr (W > 1) {
+        // each warp's choices in order (key 0 past its experts); lane w < W walks warp w's
+        cand[warp * 32 + lane] = lane < a.k ? my_key : 0u;
+        cand[(W + warp) * 32 + lane] = my_id;
+        __syncthreads();
+        if (warp > 0)
+            return;
+        int at = 0;
+        auto head = [&]() {
+            b1 = lane < W && at < 32 ? cand[lane * 32 + at] : 0u;
+            e1 = lane < W && at < 32 ? static_cast<int>(cand[(W + lane) * 32 + at]) : 0;
+        };
+        head();
+        rounds([&](uint32_t, int) {
+            ++at;
+            head();
+        });
     }
 
     float w = 0.f;
@@ -201,8 +316,10 @@ __device__ void route_token(const MoeRouteArgs& a, int64_t t, int lane, float* v
         float m = warp_max(xj);
         if (sigmoid)
             m = fminf(m, 0.f);
-        if (chosen)
-            w = sigmoid ? 1.0f / (expf(m) + expf(m - xj)) : expf(xj - m);
+        if (chosen) {
+            const float z = expf(sigmoid ? m - xj : xj - m);
+            w = sigmoid ? 1.0f / (expf(m) + z) : z;
+        }
         const float total = warp_sum(w);
         w = chosen ? w / total : 0.f;
     } else if (chosen) {
@@ -214,31 +331,53 @@ __device__ void route_token(const MoeRouteArgs& a, int64_t t, int lane, float* v
     }
 }
 
-template <typename TL, int NI>
-__global__ void __launch_bounds__(256) moe_route_kernel(MoeRouteArgs a)
+constexpr int kRouteWarps = 4;  // of a block: on one token, or a token each
+
+template <typename TL, int W, int Q>
+__global__ void __launch_bounds__(32 * kRouteWarps) moe_route_kernel(MoeRouteArgs a)
 {
     pdl_launch_dependents();
     pdl_wait();
-    extern __shared__ float route_vals[];  // [warps][E] with groups
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * nw + warp; t < a.T;
-         t += static_cast<int64_t>(gridDim.x) * nw)
-        route_token<TL, NI>(a, t, lane, route_vals + warp * a.E);
+    extern __shared__ __align__(16) uint32_t route_smem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if constexpr (W > 1) {
+        for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+            route_token<TL, W, Q>(a, t, warp, lane, route_smem);
+            __syncthreads();
+        }
+    } else {
+        uint32_t* mine = route_smem + warp * route_words<1>(a.E, a.n_group > 1);
+        for (int64_t t = static_cast<int64_t>(blockIdx.x) * kRouteWarps + warp; t < a.T;
+             t += static_cast<int64_t>(gridDim.x) * kRouteWarps) {
+            route_token<TL, 1, Q>(a, t, 0, lane, mine);
+            __syncwarp();
+        }
+    }
+}
+
+template <typename TL, int W, int Q>
+cudaError_t launch_route_as(const MoeRouteArgs& a, cudaStream_t s)
+{
+    const int64_t blocks = W > 1 ? a.T : (a.T + kRouteWarps - 1) / kRouteWarps;
+    const int words = route_words<W>(a.E, a.n_group > 1) * (W > 1 ? 1 : kRouteWarps);
+    return launch_pdl(moe_route_kernel<TL, W, Q>, static_cast<int>(blocks < 65535 ? blocks : 65535),
+                      32 * kRouteWarps, sizeof(uint32_t) * words, s, a);  // (at most 32 KB)
 }
 
 template <typename TL>
-cudaError_t launch_route_type(const MoeRouteArgs& a, int grid, int warps, cudaStream_t s)
+cudaError_t launch_route_type(const MoeRouteArgs& a, int sms, cudaStream_t s)
 {
-    const size_t smem = a.n_group > 1 ? sizeof(float) * a.E * warps : 0;
-    if (a.E <= 128)
-        return launch_pdl(moe_route_kernel<TL, 4>, grid, 32 * warps, smem, s, a);
-    if (a.E <= 256)
-        return launch_pdl(moe_route_kernel<TL, 8>, grid, 32 * warps, smem, s, a);
-    if (a.E <= 384)
-        return launch_pdl(moe_route_kernel<TL, 12>, grid, 32 * warps, smem, s, a);
-    if (a.E <= 512)
-        return launch_pdl(moe_route_kernel<TL, 16>, grid, 32 * warps, smem, s, a);
-    return launch_pdl(moe_route_kernel<TL, 32>, grid, 32 * warps, smem, s, a);
+    auto aligned = [](const void* p, int64_t step, int by) {
+        return reinterpret_cast<uintptr_t>(p) % by == 0 && step % by == 0;
+    };
+    const bool quads = a.E % 4 == 0 &&
+                       aligned(a.logits, a.ld * static_cast<int64_t>(sizeof(TL)), 4 * sizeof(TL)) &&
+                       aligned(a.bias, 0, 16);
+    // four warps a token while that leaves SMs with little to do
+    const bool few = a.T <= 4 * static_cast<int64_t>(sms);
+    if (few)
+        return quads ? launch_route_as<TL, kRouteWarps, 4>(a, s) : launch_route_as<TL, kRouteWarps, 1>(a, s);
+    return quads ? launch_route_as<TL, 1, 4>(a, s) : launch_route_as<TL, 1, 1>(a, s);
 }
 
 // Gradient of the weights at the logits, one warp per token.  With g = dL/dw
@@ -246,21 +385,25 @@ cudaError_t launch_route_type(const MoeRouteArgs& a, int grid, int warps, cudaSt
 //   sigmoid  dx_i = w_i (1 - s_i) (g_i - r)      softmax, renormalised  dx_i = w_i (g_i - r)
 //   softmax  dx_i = [i chosen] w_i g_i - p_i sum_j g_j w_j
 // where r = sum_j g_j w_j / scale when renormalised, else 0.  All but the last
-// are zero outside the chosen experts.  The row is put together in shared
-// memory and written once.
+// are zero outside the chosen experts.  Bound by the row that is written: it is
+// filled with what an expert that was not chosen gets, then lane j writes the
+// chosen expert j over it.
 template <typename TL>
-__global__ void __launch_bounds__(256) moe_route_backward_kernel(MoeRouteBwdArgs a)
+__global__ void __launch_bounds__(128) moe_route_backward_kernel(MoeRouteBwdArgs a)
 {
     pdl_launch_dependents();
     pdl_wait();
-    extern __shared__ float bwd_rows[];  // [warps][E]
+    extern __shared__ float bwd_rows[];  // [warps][E]: exponentials (softmax, not renormalised)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    float* out = bwd_rows + warp * a.E;
+    float* ex = bwd_rows + warp * a.E;
     const bool sigmoid = a.scoring == CHORD_SCORE_SIGMOID;
     const bool dense = !sigmoid && !a.renorm;
+    constexpr int kVec = 16 / sizeof(TL);
+    const bool vec = a.E % kVec == 0 && reinterpret_cast<uintptr_t>(a.d_logits) % 16 == 0;
     for (int64_t t = static_cast<int64_t>(blockIdx.x) * nw + warp; t < a.T;
          t += static_cast<int64_t>(gridDim.x) * nw) {
         const TL* row = static_cast<const TL*>(a.logits) + t * a.ld;
+        TL* dst = static_cast<TL*>(a.d_logits) + t * a.E;
         int id = -1;
         float g = 0.f, w = 0.f;
         if (lane < a.k) {
@@ -272,6 +415,29 @@ __global__ void __launch_bounds__(256) moe_route_backward_kernel(MoeRouteBwdArgs
                 w = 0.f;
             }
         }
+        float top = -INFINITY, f = 0.f;
+        if (dense) {
+            for (int e0 = lane; e0 < a.E; e0 += 256) {
+                TL raw[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (e0 + 32 * i < a.E)
+                        raw[i] = row[e0 + 32 * i];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (e0 + 32 * i < a.E) {
+                        const float x = clamp_logit(to_f32<TL>(raw[i]));
+                        ex[e0 + 32 * i] = x;
+                        top = fmaxf(top, x);
+                    }
+            }
+        } else if (vec) {
+            for (int e = kVec * lane; e < a.E; e += kVec * 32)
+                *reinterpret_cast<uint4*>(dst + e) = make_uint4(0u, 0u, 0u, 0u);
+        } else {
+            for (int e = lane; e < a.E; e += 32)
+                dst[e] = from_f32<TL>(0.f);
+        }
         const float gw = w != 0.f ? g * w : 0.f;
         const float dot = warp_sum(gw);
         float v = gw;
@@ -280,42 +446,31 @@ __global__ void __launch_bounds__(256) moe_route_backward_kernel(MoeRouteBwdArgs
         if (sigmoid && w != 0.f)
             v *= 1.0f / (1.0f + expf(load_logit(row + id)));  // 1 - s
         if (dense) {
-            float top = -INFINITY;
-            for (int e = lane; e < a.E; e += 32) {
-                const float x = load_logit(row + e);
-                out[e] = x;
-                top = fmaxf(top, x);
-            }
             top = warp_max(top);
             if (top == -INFINITY)
                 top = 0.f;
             float sum = 0.f;
+#pragma unroll 4
             for (int e = lane; e < a.E; e += 32) {
-                const float p = expf(out[e] - top);
-                out[e] = p;
+                const float p = expf(ex[e] - top);
+                ex[e] = p;
                 sum += p;
             }
             sum = warp_sum(sum);
-            const float f = sum > 0.f ? -dot / sum : 0.f;
+            f = sum > 0.f ? -dot / sum : 0.f;
+#pragma unroll 4
             for (int e = lane; e < a.E; e += 32)
-                out[e] *= f;
-        } else {
-            for (int e = lane; e < a.E; e += 32)
-                out[e] = 0.f;
+                dst[e] = from_f32<TL>(ex[e] * f);
         }
-        __syncwarp();
+        __syncwarp();  // the fill comes before the chosen experts' writes
         if (id >= 0)
-            atomicAdd(out + id, v);
-        __syncwarp();
-        TL* dst = static_cast<TL*>(a.d_logits) + t * a.E;
-        for (int e = lane; e < a.E; e += 32)
-            dst[e] = from_f32<TL>(out[e]);
+            dst[id] = from_f32<TL>(dense ? v + ex[id] * f : v);
         __syncwarp();
     }
 }
 
-// Blocks of one warp spread a small batch over the SMs; larger ones take 8.
-int warps_per_block(int64_t T, int sms) { return T <= 8 * static_cast<int64_t>(sms) ? 1 : 8; }
+// Blocks of one warp spread a small batch over the SMs; larger ones take 4.
+int warps_per_block(int64_t T, int sms) { return T <= 8 * static_cast<int64_t>(sms) ? 1 : 4; }
 
 int blocks_for(int64_t T, int warps)
 {
@@ -327,14 +482,14 @@ int blocks_for(int64_t T, int warps)
 
 cudaError_t launch_moe_route(const MoeRouteArgs& a, int sms, cudaStream_t s)
 {
-    const int warps = warps_per_block(a.T, sms), grid = blocks_for(a.T, warps);
-    return with_type(a.type, [&](auto v) { return launch_route_type<decltype(v)>(a, grid, warps, s); });
+    return with_type(a.type, [&](auto v) { return launch_route_type<decltype(v)>(a, sms, s); });
 }
 
 cudaError_t launch_moe_route_backward(const MoeRouteBwdArgs& a, int sms, cudaStream_t s)
 {
     const int warps = warps_per_block(a.T, sms), grid = blocks_for(a.T, warps);
-    const size_t smem = sizeof(float) * a.E * warps;
+    const bool dense = a.scoring == CHORD_SCORE_SOFTMAX && !a.renorm;
+    const size_t smem = dense ? sizeof(float) * a.E * warps : 0;
     return with_type(a.type, [&](auto v) {
         return launch_pdl(moe_route_backward_kernel<decltype(v)>, grid, 32 * warps, smem, s, a);
     });
