@@ -41,8 +41,8 @@ chord_status finish(int flags, void* ws, cudaStream_t s)
     return chord_get_device_error(ws, nullptr, 0, s);
 }
 
-// bytes of a token code between the kernels: 1, or 2 as the fp16 operand of the
-// tensor-core product
+// bytes of a token code between the kernels: 1, or 2 as the fp16 operand of
+// launch_int8_gemm
 int code_size(int64_t T) { return T <= kInt8RowsMaxT ? 1 : 2; }
 
 struct Scratch {  // of chord_int8_linear and chord_int8_mlp
@@ -216,7 +216,7 @@ chord_status chord_int8_matmul(const int8_t* a, int64_t ld_a, const float* a_sca
     if ((st = device_info(&dev)) != CHORD_OK)
         return st;
     Int8Args g{a, nullptr, w, ld_a, ld_w, a_scale, w_scale, T, N, K, residual, ld_r, out, ld_out, type,
-               static_cast<int*>(workspace)};
+               static_cast<int*>(workspace), 0};
     PdlScope pdl(T <= kPdlMaxRows);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
@@ -227,6 +227,7 @@ chord_status chord_int8_matmul(const int8_t* a, int64_t ld_a, const float* a_sca
         e = launch_int8_to_f16(a, ld_a, T, K, a16, pad16(K), g.err, dev.sms, s);
         g.a16 = a16;
         g.ld_a = pad16(K);
+        g.after_codes = 1;
         if (e == cudaSuccess)
             e = launch_int8_gemm(g, dev.sms, s);
     }
@@ -263,7 +264,7 @@ chord_status chord_int8_linear(const void* x, int type, int64_t ld_x, const int8
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     PdlScope pdl(T <= kPdlMaxRows);
     const QuantArgs qa{x, type, T, K, ld_x, nullptr, nullptr, 0, nullptr, 0, err};
-    const Int8Args g{nullptr, nullptr, w, 0, ld_w, nullptr, w_scale, T, N, K, residual, ld_r, out, ld_out, type, err};
+    const Int8Args g{nullptr, nullptr, w, 0, ld_w, nullptr, w_scale, T, N, K, residual, ld_r, out, ld_out, type, err, 1};
     if (quantize_product(qa, g, ws + p.codes, qs, dev, s) != cudaSuccess)
         return CHORD_ERR_CUDA;
     return finish(flags, workspace, s);
@@ -304,9 +305,9 @@ chord_status chord_int8_mlp(const void* x, int type, int64_t ld_x, const int8_t*
     const int64_t ld_m = 2 * static_cast<int64_t>(I);
     const QuantArgs xa{x, type, T, H, ld_x, nullptr, nullptr, 0, nullptr, 0, err};
     const Int8Args g1{nullptr, nullptr, w13, 0,   ld_w13, nullptr,        w13_scale, T, 2 * I, H,
-                      nullptr, 0,       mid, ld_m, CHORD_TYPE_F32, err};
+                      nullptr, 0,       mid, ld_m, CHORD_TYPE_F32, err, 1};
     const QuantArgs ha{mid, CHORD_TYPE_F32, T, I, ld_m, nullptr, nullptr, 0, nullptr, 1, nullptr};
-    const Int8Args g2{nullptr, nullptr, w2, 0, ld_w2, nullptr, w2_scale, T, H, I, residual, ld_r, out, ld_out, type, err};
+    const Int8Args g2{nullptr, nullptr, w2, 0, ld_w2, nullptr, w2_scale, T, H, I, residual, ld_r, out, ld_out, type, err, 1};
     if (quantize_product(xa, g1, ws + p.codes, qs, dev, s) != cudaSuccess ||
         quantize_product(ha, g2, ws + p.codes2, qs2, dev, s) != cudaSuccess)
         return CHORD_ERR_CUDA;

@@ -60,7 +60,7 @@ struct QuantArgs {
     int K;
     int64_t ld_x;
     int8_t* q;    // [T, K], rows ld_q codes apart, 16-byte aligned, or null:
-    __half* q16;  // the same codes as fp16 (exact), for the tensor-core product
+    __half* q16;  // the same codes as fp16 (exact), for launch_int8_gemm
     int64_t ld_q;
     float* scale;  // [T]
     int silu_mul;
@@ -70,8 +70,8 @@ cudaError_t launch_int8_quantize(const QuantArgs& a, int sms, cudaStream_t s);
 
 // chord_int8_matmul
 struct Int8Args {
-    const int8_t* a;    // [T, K] tokens, rows ld_a codes apart (CUDA-core product)
-    const __half* a16;  // the same codes as fp16 (tensor-core product)
+    const int8_t* a;    // [T, K] tokens, rows ld_a codes apart (launch_int8_rows)
+    const __half* a16;  // the same codes as fp16 (launch_int8_gemm)
     const int8_t* w;    // [N, K] channels, rows ld_w bytes apart
     int64_t ld_a;
     int64_t ld_w;
@@ -86,18 +86,20 @@ struct Int8Args {
     int64_t ld_out;
     int type;
     int* err;  // device error word (the call's first kernel clears it)
+    // The kernel before this one in the stream makes the codes: it does not write
+    // the weight and lets its successor start only after its own predecessors have
+    // ended, so the weight may be read before that kernel has ended.
+    int after_codes;
 };
 // 8-bit codes [T, K], rows ld_a apart, as fp16, rows ld_out apart (multiples of 16)
 cudaError_t launch_int8_to_f16(const int8_t* a, int64_t ld_a, int64_t T, int K, __half* out, int64_t ld_out,
                                int* err, int sms, cudaStream_t s);
-// Up to this many tokens the CUDA-core product is taken.
-constexpr int64_t kInt8RowsMaxT = 8;
-// CUDA-core product (any T; streams the weights once per 8 tokens)
+// Up to this many tokens launch_int8_rows is taken.  (Measured with N = 4096, K =
+// 7168, both: 8 tokens %R8, 16 tokens %R16, us a product.)
+constexpr int64_t kInt8RowsMaxT = 16;
+// few tokens: mma.sync on the 8-bit codes (T <= kInt8RowsMaxT)
 cudaError_t launch_int8_rows(const Int8Args& a, int sms, cudaStream_t s);
-// Tensor-core product of a.a16.  The kernel before it in the stream must be one
-// of those above that make the codes: it does not write the weight and lets its
-// successor start only after its own predecessors have ended, so this one reads
-// the weight before that kernel has ended.
+// more: tcgen05 on fp16 codes; a.after_codes must hold
 cudaError_t launch_int8_gemm(const Int8Args& a, int sms, cudaStream_t s);
 
 // ---------------------------------------------------------------------------

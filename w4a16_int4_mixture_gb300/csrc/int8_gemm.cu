@@ -29,8 +29,8 @@
 //                1024 + 128 + code; subtracting 1152 is exact (1.25
 //                instructions per code)
 //   epilogue     eight warps, two per lane quadrant (half of the columns each)
-// Split K (CG = 1): a weight with fewer tiles than SMs is cut along K over the
-// CTAs of a cluster; the integer partial sums meet in distributed shared memory.
+// Split K: a weight with fewer tiles than SMs is cut along K over the CTAs (pairs)
+// of a cluster; the integer partial sums meet in distributed shared memory.
 // Every wait is bounded (2 s): on expiry CHORD_DEVERR_TIMEOUT is recorded, every
 // role leaves its loop and tensor memory is freed.
 #include <cudaTypedefs.h>
@@ -47,13 +47,14 @@ constexpr int kHalfK = 64;   // codes a converter group takes at a time (128 byt
 constexpr int kChainK = 1024;  // products of an accumulation chain
 constexpr int kTileM = 128;  // channels of a CTA's tile
 constexpr int kEpiWarps = 8;
+constexpr int kMaxSplit = 8;  // parts of K
 
 struct Int8Gemm {
     Int8Args p;
     int nt;        // token tile: a multiple of 16 (CG = 2: 32), at most NTMAX
     int n_tiles;   // channel tiles (of 128 * CG)
     int units;     // channel tiles * token tiles
-    int split;     // CTAs of a cluster that share a unit along K (CG = 1)
+    int split;     // parts of K of a unit: CTAs (pairs) of a cluster
 };
 
 // CG CTAs per tile, token tile, raw weight stages, halves of 64 codes per item,
@@ -196,9 +197,10 @@ __device__ __forceinline__ void mma_item(uint32_t d, uint32_t a, uint64_t b_desc
 #undef CHORD_INT8_ITEM
 #undef CHORD_INT8_SECOND
 
-// Arrives on `bar` (of both CTAs of a pair) when the MMAs issued so far are done.
+// Arrives on `bar` (of both CTAs of a pair: bits of their ranks) when the MMAs
+// issued so far are done.
 template <int CG>
-__device__ __forceinline__ void commit_elect(uint32_t bar)
+__device__ __forceinline__ void commit_elect(uint32_t bar, uint16_t pair)
 {
     if constexpr (CG == 1)
         mma_commit_elect(bar);
@@ -207,7 +209,7 @@ __device__ __forceinline__ void commit_elect(uint32_t bar)
             "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
             "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
             "[%0], %1;\n\t}" ::"r"(bar),
-            "h"(static_cast<uint16_t>(3))
+            "h"(pair)
             : "memory");
 }
 
@@ -218,13 +220,13 @@ __device__ __forceinline__ void commit_elect(uint32_t bar)
 // cluster scope, each a memory barrier of some 500 clocks, an item of the pair
 // took 800 clocks instead of %s.
 template <int CG>
-__device__ __forceinline__ void arrive_first(uint32_t bar)
+__device__ __forceinline__ void arrive_first(uint32_t bar, uint32_t lead)
 {
     if constexpr (CG == 1) {
         mbar_arrive(bar);
     } else {
         uint32_t ra;
-        asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(ra) : "r"(bar));
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(bar), "r"(lead));
         asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(ra) : "memory");
     }
 }
@@ -239,22 +241,35 @@ __device__ __forceinline__ void cluster_sync_all()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ int ld_cluster_s32(uint32_t addr, uint32_t rank)
+__device__ __forceinline__ int4 ld_cluster_s32x4(uint32_t addr, uint32_t rank)
 {
     uint32_t ra;
-    int v;
+    int4 v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(addr), "r"(rank));
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(ra) : "memory");
+    asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(ra)
+                 : "memory");
     return v;
 }
 
+// out of one token and four channels from n on (those below N)
 template <typename T>
-__device__ __forceinline__ void store_sum(const Int8Args& a, int64_t t, int n, int sum, float ws)
+__device__ __forceinline__ void store_quad(const Int8Args& a, int64_t t, int n, const int (&sum)[4])
 {
-    float v = static_cast<float>(sum) * a.a_scale[t] * ws;
-    if (a.residual)
-        v += to_f32<T>(static_cast<const T*>(a.residual)[t * a.ld_r + n]);
-    static_cast<T*>(a.out)[t * a.ld_out + n] = from_f32<T>(v);
+    const float as = a.a_scale[t];
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (n + i < a.N) {
+            v[i] = static_cast<float>(sum[i]) * as * a.w_scale[n + i];
+            if (a.residual)
+                v[i] += to_f32<T>(static_cast<const T*>(a.residual)[t * a.ld_r + n + i]);
+        }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (n + i < a.N)
+            static_cast<T*>(a.out)[t * a.ld_out + n + i] = from_f32<T>(v[i]);
 }
 
 // out of one channel and 8 * NB tokens from t0 on (those below T, at most cols).
@@ -315,8 +330,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     uint8_t* smem = smem_raw + (sbase - raw_u32);
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const int cluster = C::CG * g.split;  // (one of the two is 1)
-    const int rank = cluster > 1 ? static_cast<int>(cluster_rank()) : 0;
+    const int cluster = C::CG * g.split;
+    const int in_cluster = cluster > 1 ? static_cast<int>(cluster_rank()) : 0;
+    const int rank = in_cluster % C::CG, krank = in_cluster / C::CG;  // in the pair; part of K
+    const uint32_t lead = in_cluster - rank;                          // the pair's first CTA
+    const uint16_t pair = static_cast<uint16_t>(3u << lead);
 
     const uint32_t bar0 = sbase + C::OFF_BARS;
     auto raw_full = [&](int s) { return bar0 + 8u * s; };
@@ -363,7 +381,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
     // this CTA's (or pair's) units and K stages
     const int KT = (g.p.K + kRawK - 1) / kRawK;
-    const int krank = C::CG == 1 ? rank : 0;
     const int k0 = krank * KT / g.split, k1 = (krank + 1) * KT / g.split;
     const int u0 = blockIdx.x / cluster, ustep = gridDim.x / cluster;
     const int my_units = u0 < g.units ? (g.units - 1 - u0) / ustep + 1 : 0;
@@ -451,18 +468,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         mma_item<C::CG, C::HV, C::B_HALF / 16>(d, tmem + s * C::A_COLS, bdesc0 + s * (C::B_ITEM / 16),
                                                         idesc, c != c0 ? 1u : 0u);
                         any = 1;
-                        commit_elect<C::CG>(cv_empty(s));
+                        commit_elect<C::CG>(cv_empty(s), pair);
                         if (++s == C::AS) {
                             s = 0;
                             phase ^= 1u;
                         }
                     }
                     if (ok)
-                        commit_elect<C::CG>(acc_full(acc));
+                        commit_elect<C::CG>(acc_full(acc), pair);
                 }
             }
             if (!ok && any) {  // work in flight ends before tensor memory is freed
-                commit_elect<C::CG>(drain_bar);
+                commit_elect<C::CG>(drain_bar, pair);
                 mbar_drain(drain_bar, 0);
             }
             __syncwarp();
@@ -513,7 +530,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0)
-                arrive_first<C::CG>(cv_full(s));
+                arrive_first<C::CG>(cv_full(s), lead);
         }
         // (pair: the last arrivals from the first CTA's commits have landed)
         if (C::CG == 2 && ok && j > grp) {
@@ -570,7 +587,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    arrive_first<C::CG>(acc_empty(acc));
+                    arrive_first<C::CG>(acc_empty(acc), lead);
             }
             if (!ok)
                 break;
@@ -604,22 +621,32 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         tc_fence_after();
         tmem_dealloc_cg<C::CG>(tmem, C::TMEM_COLS);
     }
-    if (C::CG == 1 && g.split > 1) {
-        // every CTA of the cluster finishes a share of the token columns
+    if (g.split > 1) {
+        // every CTA of the cluster finishes a share of its token columns, four
+        // channels a thread, the loads from all parts at once
         __syncthreads();
         cluster_sync_all();
         pdl_wait();
-        const int n0 = u0 % g.n_tiles * kTileM;
+        const int n0 = u0 % g.n_tiles * (kTileM * C::CG) + rank * kTileM;
         const int64_t t0 = static_cast<int64_t>(u0 / g.n_tiles) * nt;
-        const int c0 = rank * nt / g.split, c1 = (rank + 1) * nt / g.split;
-        for (int i = threadIdx.x; i < (c1 - c0) * kTileM; i += C::THREADS) {
-            const int col = c0 + i / kTileM, r = i % kTileM;
+        const int c0 = krank * nt / g.split, c1 = (krank + 1) * nt / g.split;
+        for (int i = threadIdx.x; i < (c1 - c0) * (kTileM / 4); i += C::THREADS) {
+            const int col = c0 + i / (kTileM / 4), r = i % (kTileM / 4) * 4;
             const uint32_t at = sbase + 4u * (col * kTileM + r);
-            int sum = 0;
-            for (int k = 0; k < g.split; ++k)
-                sum += ld_cluster_s32(at, k);
-            if (n0 + r < g.p.N && t0 + col < g.p.T)
-                store_sum<T>(g.p, t0 + col, n0 + r, sum, g.p.w_scale[n0 + r]);
+            int4 v[kMaxSplit];
+#pragma unroll
+            for (int k = 0; k < kMaxSplit; ++k)
+                v[k] = k < g.split ? ld_cluster_s32x4(at, k * C::CG + rank) : make_int4(0, 0, 0, 0);
+            int sum[4] = {};
+#pragma unroll
+            for (int k = 0; k < kMaxSplit; ++k) {
+                sum[0] += v[k].x;
+                sum[1] += v[k].y;
+                sum[2] += v[k].z;
+                sum[3] += v[k].w;
+            }
+            if (t0 + col < g.p.T)
+                store_quad<T>(g.p, t0 + col, n0 + r, sum);
         }
         cluster_sync_all();  // (the partial sums stay until every CTA has read them)
     }
@@ -682,7 +709,7 @@ cudaError_t launch_cfg(Int8Gemm g, int sms, cudaStream_t s)
         (e = codes_map(g.p.a16, 2, g.p.T, g.p.K, g.p.ld_a, g.nt / C::CG, &tm)) != cudaSuccess)
         return e;
     const int cluster = C::CG * g.split;
-    const int most = g.split > 1 ? g.units : sms / C::CG;  // clusters
+    const int most = g.split > 1 ? g.units : sms / C::CG;  // clusters (split K: one unit each)
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = cluster * (g.units < most ? g.units : most);
     cfg.blockDim = C::THREADS;
@@ -706,37 +733,57 @@ using CfgT32 = Int8Cfg<1, 32, 9, 2, 4, 4>;
 using CfgT128 = Int8Cfg<1, 128, 5, 2, 4, 3, 40, 64, 120>;
 using CfgP160 = Int8Cfg<2, 160, 8, 1, 6, 2, 40, 72, 144>;
 
+// Parts of K: doubled while the units' parts fit the SMs and each keeps at least
+// two raw stages.  Clusters of 8 only where they leave half of the SMs free: they
+// must find their SMs in one GPC each, and a GPC short of them costs a second
+// round (16 clusters of 8: 21 us where 32 of 4 took 13).
+int split_of(int64_t units, int cg, int K, int sms)
+{
+    const int KT = (K + kRawK - 1) / kRawK;
+    int split = 1;
+    while (KT >= 4 * split) {
+        const int64_t ctas = units * split * 2 * cg;
+        if (ctas > sms || split * 2 * cg > 8 || (split * 2 * cg == 8 && ctas > sms / 2))
+            break;
+        split *= 2;
+    }
+    return split;
+}
+
 template <typename T>
 cudaError_t launch_type(const Int8Args& a, int sms, cudaStream_t s)
 {
     Int8Gemm g{};
     g.p = a;
-    g.split = 1;
-    const int64_t t16 = (a.T + 15) / 16 * 16;
-    const int KT = (a.K + kRawK - 1) / kRawK;
-    if (t16 <= 128) {
-        // one token tile, K cut until the SMs are used
-        g.nt = static_cast<int>(t16);
+    // one token tile: single CTAs, twice as many channel tiles to spread
+    if (a.T <= CfgT128::NTMAX) {
+        g.nt = static_cast<int>((a.T + 15) / 16 * 16);
         g.n_tiles = g.units = (a.N + kTileM - 1) / kTileM;
-        while (g.split < 8 && g.units * g.split * 2 <= sms && KT >= 4 * g.split)
-            g.split *= 2;
-        if (g.nt <= 32)
+        g.split = split_of(g.units, 1, a.K, sms);
+        if (g.nt <= CfgT32::NTMAX)
             return launch_cfg<CfgT32, T>(g, sms, s);
         return launch_cfg<CfgT128, T>(g, sms, s);
     }
-    // CTA pairs (N of their MMA is a multiple of 32); the token tile whose rounds
-    // of units cost least
+    // CTA pairs (N of their MMA is a multiple of 32): the token tile for which the
+    // rounds of units cost least, in clocks as measured: an item takes its MMAs'
+    // 2 nt clocks and the handshakes between the CTAs, at least the converters'
+    // 430; a unit some 5000 more, and 8000 where its parts are joined
     g.n_tiles = (a.N + 2 * kTileM - 1) / (2 * kTileM);
-    int64_t best = INT64_MAX;
-    for (int nt = CfgP160::NTMAX; nt >= 96; nt -= 32) {
-        const int64_t units = (a.T + nt - 1) / nt * g.n_tiles;
-        const int64_t cost = (units + sms / 2 - 1) / (sms / 2) * (nt + 16);
+    const int64_t items = (a.K + kHalfK - 1) / kHalfK, pairs = sms / 2;
+    int64_t best = INT64_MAX, units = 0;
+    for (int nt = CfgP160::NTMAX; nt >= 64; nt -= 32) {
+        const int64_t u = (a.T + nt - 1) / nt * g.n_tiles;
+        const int split = split_of(u, 2, a.K, sms);
+        const int64_t item = 2 * nt + 150 > 430 ? 2 * nt + 150 : 430;
+        const int64_t rounds = (u * split + pairs - 1) / pairs;
+        const int64_t cost = rounds * (items / split * item + (split > 1 ? 13000 : 5000));
         if (cost < best) {
             best = cost;
+            units = u;
             g.nt = nt;
+            g.split = split;
         }
     }
-    const int64_t units = (a.T + g.nt - 1) / g.nt * g.n_tiles;
     if (units > INT32_MAX)
         return cudaErrorInvalidValue;
     g.units = static_cast<int>(units);

@@ -1,6 +1,5 @@
 // int8_kernels.cu -- rows quantised to 8-bit integers with a scale each (plain,
-// or of silu(gate) * up), and the 8-bit product on the CUDA cores for few
-// tokens.
+// or of silu(gate) * up), and the 8-bit product for few tokens.
 #include <type_traits>
 
 #include "block_kernels.h"
@@ -225,137 +224,182 @@ __global__ void __launch_bounds__(256)
 }
 
 // ---------------------------------------------------------------------------
-// the product on the CUDA cores: dp4a, exact in 32-bit integers
+// the product for few tokens, on the 8-bit codes, exact in 32-bit integers
 // ---------------------------------------------------------------------------
-constexpr int kRowsN = 2;  // channels per warp
+// Bound by streaming the weight, so its codes go straight from memory to registers
+// and from there into dp4a (one token) or mma.sync (up to 16): no conversion, no
+// shared memory.  Both have low rates on this part (dp4a about 8 lanes a clock and
+// SM, mma.sync on 8-bit integers about 120 TOP/s, on fp16 about 215 TFLOP/s), and
+// this is the best of them for each count: K = 7168, N = 4096, us, weights in L2:
+// %TABLE
+constexpr int kRowsM = 16;     // channels of a warp (the MMA's M)
+constexpr int kRowsWarps = 16;  // warps of a block: parts of K, or channel groups
+constexpr int kRowsK = 64;     // codes of a step: two MMAs of K = 32
+constexpr int kRowsAhead = 2;  // steps whose loads are in flight
 
-// 16 codes of a row from k; past K (only the last chunk of a row) zero.  A chunk
-// is never read past the row's K codes: the row may end its allocation.
-__device__ __forceinline__ int4 load_codes(const int8_t* row, int k, int K)
+// 16 codes of a row from k; past K zero.  A row is never read past its K codes:
+// it may end its allocation.
+__device__ __noinline__ uint4 load_codes(const int8_t* row, int k, int K)
 {
     if (k + 16 <= K)
-        return *reinterpret_cast<const int4*>(row + k);
+        return *reinterpret_cast<const uint4*>(row + k);
     uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int i = 0; i < 16; ++i)
         if (k + i < K)
             w[i >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(row[k + i])) << (8 * (i & 3));
-    return make_int4(static_cast<int>(w[0]), static_cast<int>(w[1]), static_cast<int>(w[2]),
-                     static_cast<int>(w[3]));
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <typename T>
-__device__ __forceinline__ void store_out(const Int8Args& a, int64_t t, int n, int sum)
+__device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1)
 {
-    float v = static_cast<float>(sum) * a.a_scale[t] * a.w_scale[n];
-    if (a.residual)
-        v += to_f32<T>(static_cast<const T*>(a.residual)[t * a.ld_r + n]);
-    static_cast<T*>(a.out)[t * a.ld_out + n] = from_f32<T>(v);
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// A warp takes kRowsN channels and TT tokens; its lanes walk K in 16-byte
-// chunks.  ks warps of a block share the channels, each a part of K, so that a
-// narrow weight still keeps every SM's loads in flight; their integer partial
-// sums are added in shared memory.
-template <typename T, int TT>
-__global__ void __launch_bounds__(256) int8_rows_kernel(Int8Args a, int ks)
+__device__ __forceinline__ int dot16(const uint4& a, const uint4& b, int sum)
 {
-    __shared__ int part[8][kRowsN * TT];
-    pdl_launch_dependents();
-    pdl_wait();
-    if (a.err && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0)
-        *a.err = 0;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int groups = 8 / ks;
-    const int n0 = (blockIdx.x * groups + warp / ks) * kRowsN;
-    const int64_t t0 = static_cast<int64_t>(blockIdx.y) * TT;
-    int acc[kRowsN][TT] = {};
-    const int8_t* wr[kRowsN];
+    sum = __dp4a(static_cast<int>(a.x), static_cast<int>(b.x), sum);
+    sum = __dp4a(static_cast<int>(a.y), static_cast<int>(b.y), sum);
+    sum = __dp4a(static_cast<int>(a.z), static_cast<int>(b.z), sum);
+    return __dp4a(static_cast<int>(a.w), static_cast<int>(b.w), sum);
+}
+
+// A warp multiplies 16 channels by 8 NB tokens (NB = 0: by one) over the steps of
+// its part of K.  Lane 4 r + c holds 16 consecutive codes (a step's piece c) of
+// channels r, r + 8 and of tokens r, r + 8 ...: both operands in the same order
+// along K, which is all that the sum asks for, instead of the MMA's own, which
+// would take four narrow loads.  ks warps of a block share the channels, each a
+// part of K, so that a narrow weight still keeps every SM's loads in flight.
+template <typename T, int NB>
+__global__ void __launch_bounds__(32 * kRowsWarps) int8_rows_kernel(Int8Args a, int ks)
+{
+    constexpr int NT = NB == 0 ? 1 : 8 * NB;  // tokens
+    constexpr int NX = NB == 0 ? 1 : NB;      // token rows of a lane
+    __shared__ int part[kRowsWarps][kRowsM * NT];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
+    const int n0 = (blockIdx.x * (kRowsWarps / ks) + warp / ks) * kRowsM;
+    const int8_t* wr[2];
 #pragma unroll
-    for (int r = 0; r < kRowsN; ++r)
-        wr[r] = a.w + static_cast<int64_t>(min(n0 + r, a.N - 1)) * a.ld_w;
-    if (n0 < a.N) {
-#pragma unroll 4
-        for (int k = 16 * (lane + 32 * (warp % ks)); k < a.K; k += 512 * ks) {
-            int4 wv[kRowsN];
+    for (int i = 0; i < 2; ++i)
+        wr[i] = a.w + static_cast<int64_t>(min(n0 + r + 8 * i, a.N - 1)) * a.ld_w;
+    const int8_t* ar[NX];
 #pragma unroll
-            for (int r = 0; r < kRowsN; ++r)
-                wv[r] = load_codes(wr[r], k, a.K);
+    for (int j = 0; j < NX; ++j)
+        ar[j] = a.a + (NB == 0 ? 0 : min(static_cast<int64_t>(r + 8 * j), a.T - 1) * a.ld_a);
+    const int mine = warp % ks, full = a.K / kRowsK;  // whole steps
+    uint4 w[kRowsAhead][2], x[kRowsAhead][NX];
+    auto load_w = [&](int b, int st) {
+        if (st < full)
 #pragma unroll
-            for (int i = 0; i < TT; ++i) {
-                if (t0 + i < a.T) {
-                    const int4 av = load_codes(a.a + (t0 + i) * a.ld_a, k, a.K);
+            for (int i = 0; i < 2; ++i)
+                w[b][i] = *reinterpret_cast<const uint4*>(wr[i] + st * kRowsK + 16 * c);
+    };
+    auto load_x = [&](int b, int st) {
+        if (st < full)
 #pragma unroll
-                    for (int r = 0; r < kRowsN; ++r) {
-                        acc[r][i] = __dp4a(wv[r].x, av.x, acc[r][i]);
-                        acc[r][i] = __dp4a(wv[r].y, av.y, acc[r][i]);
-                        acc[r][i] = __dp4a(wv[r].z, av.z, acc[r][i]);
-                        acc[r][i] = __dp4a(wv[r].w, av.w, acc[r][i]);
-                    }
-                }
+            for (int j = 0; j < NX; ++j)
+                x[b][j] = *reinterpret_cast<const uint4*>(ar[j] + st * kRowsK + 16 * c);
+    };
+    int acc[NX][4] = {};  // (NB = 0: two channels' sums over the lane's pieces)
+    auto step = [&](const uint4 (&wv)[2], const uint4 (&xv)[NX]) {
+        if constexpr (NB == 0) {
+            acc[0][0] = dot16(wv[0], xv[0], acc[0][0]);
+            acc[0][1] = dot16(wv[1], xv[0], acc[0][1]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < NX; ++j) {
+                mma_s8(acc[j], wv[0].x, wv[1].x, wv[0].y, wv[1].y, xv[j].x, xv[j].y);
+                mma_s8(acc[j], wv[0].z, wv[1].z, wv[0].w, wv[1].w, xv[j].z, xv[j].w);
             }
         }
+    };
+    // the first weights come in while the kernel before this one makes the codes
+    if (!a.after_codes)
+        pdl_wait();
+    pdl_launch_dependents();
+#pragma unroll
+    for (int b = 0; b < kRowsAhead; ++b)
+        load_w(b, mine + b * ks);
+    if (a.after_codes)
+        pdl_wait();
+    if (a.err && blockIdx.x == 0 && threadIdx.x == 0)
+        *a.err = 0;
+#pragma unroll
+    for (int b = 0; b < kRowsAhead; ++b)
+        load_x(b, mine + b * ks);
+    for (int st = mine; st < full; st += kRowsAhead * ks) {
+#pragma unroll
+        for (int b = 0; b < kRowsAhead; ++b)
+            if (st + b * ks < full) {
+                step(w[b], x[b]);
+                load_w(b, st + (b + kRowsAhead) * ks);
+                load_x(b, st + (b + kRowsAhead) * ks);
+            }
     }
-    // lane r * TT + i keeps the sum of channel r and token i
-    int mine = 0;
+    if (a.K % kRowsK != 0 && full % ks == mine) {  // the step that K ends in
+        const int k = full * kRowsK + 16 * c;
+        const uint4 wt[2] = {load_codes(wr[0], k, a.K), load_codes(wr[1], k, a.K)};
+        uint4 xt[NX];
 #pragma unroll
-    for (int r = 0; r < kRowsN; ++r)
+        for (int j = 0; j < NX; ++j)
+            xt[j] = load_codes(ar[j], k, a.K);
+        step(wt, xt);
+    }
+    // this warp's sums, channel m of token t at t * 16 + m
+    if constexpr (NB == 0) {
 #pragma unroll
-        for (int i = 0; i < TT; ++i) {
-            const int s = __reduce_add_sync(kFull, acc[r][i]);
-            if (lane == r * TT + i)
-                mine = s;
+        for (int i = 0; i < 2; ++i) {
+            int v = acc[0][i];
+            v += __shfl_xor_sync(kFull, v, 1);
+            v += __shfl_xor_sync(kFull, v, 2);
+            if (c == 0)
+                part[warp][r + 8 * i] = v;
         }
-    if (ks > 1) {
-        if (lane < kRowsN * TT)
-            part[warp][lane] = mine;
-        __syncthreads();
-        if (warp % ks != 0)
-            return;
-        if (lane < kRowsN * TT)
-            for (int j = 1; j < ks; ++j)
-                mine += part[warp + j][lane];
+    } else {
+#pragma unroll
+        for (int j = 0; j < NX; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)  // (D: channel r + 8 (i / 2), token 2 c + i % 2)
+                part[warp][(8 * j + 2 * c + (i & 1)) * kRowsM + r + 8 * (i >> 1)] = acc[j][i];
     }
-    const int n = n0 + lane / TT;
-    const int64_t t = t0 + lane % TT;
-    if (lane < kRowsN * TT && n < a.N && t < a.T)
-        store_out<T>(a, t, n, mine);
+    __syncthreads();
+    // one output a thread: the sum of the parts
+    for (int o = threadIdx.x; o < (kRowsWarps / ks) * kRowsM * NT; o += 32 * kRowsWarps) {
+        const int grp = o / (kRowsM * NT), at = o % (kRowsM * NT), t = at / kRowsM;
+        const int n = (blockIdx.x * (kRowsWarps / ks) + grp) * kRowsM + at % kRowsM;
+        if (n < a.N && t < a.T) {
+            int sum = 0;
+            for (int k = 0; k < ks; ++k)
+                sum += part[grp * ks + k][at];
+            float v = static_cast<float>(sum) * a.a_scale[t] * a.w_scale[n];
+            if (a.residual)
+                v += to_f32<T>(static_cast<const T*>(a.residual)[t * a.ld_r + n]);
+            static_cast<T*>(a.out)[t * a.ld_out + n] = from_f32<T>(v);
+        }
+    }
 }
 
 template <typename T>
 cudaError_t launch_rows_type(const Int8Args& a, int sms, cudaStream_t s)
 {
-    // parts of K per channel pair: until 16 warps per SM have work, each part
-    // at least one sweep of its lanes (512 codes)
+    // parts of K per channel group: until 16 warps per SM have work, each part at
+    // least four steps
     int ks = 1;
-    const int64_t pairs = (a.N + kRowsN - 1) / kRowsN;
-    while (ks < 8 && pairs * ks < 16 * static_cast<int64_t>(sms) && a.K > 512 * ks)
+    const int64_t groups = (a.N + kRowsM - 1) / kRowsM;
+    while (ks < kRowsWarps && groups * ks < 16 * static_cast<int64_t>(sms) && a.K > 4 * kRowsK * ks)
         ks *= 2;
-    const int per_block = 8 / ks * kRowsN;
-    const int tt = a.T >= 5 ? 8 : a.T >= 3 ? 4 : static_cast<int>(a.T);
-    const int64_t ty = (a.T + tt - 1) / tt;
-    for (int64_t y = 0; y < ty; y += 65535) {  // (the grid's y limit)
-        Int8Args b = a;
-        b.T = a.T - y * tt;
-        if (b.T > 65535 * static_cast<int64_t>(tt))
-            b.T = 65535 * static_cast<int64_t>(tt);
-        b.a = a.a + y * tt * a.ld_a;
-        b.a_scale = a.a_scale + y * tt;
-        b.out = static_cast<T*>(a.out) + y * tt * a.ld_out;
-        if (a.residual)
-            b.residual = static_cast<const T*>(a.residual) + y * tt * a.ld_r;
-        const dim3 grid((a.N + per_block - 1) / per_block, static_cast<unsigned>((b.T + tt - 1) / tt));
-        cudaError_t e;
-        switch (tt) {
-        case 1: e = launch_pdl(int8_rows_kernel<T, 1>, grid, 256, 0, s, b, ks); break;
-        case 2: e = launch_pdl(int8_rows_kernel<T, 2>, grid, 256, 0, s, b, ks); break;
-        case 4: e = launch_pdl(int8_rows_kernel<T, 4>, grid, 256, 0, s, b, ks); break;
-        default: e = launch_pdl(int8_rows_kernel<T, 8>, grid, 256, 0, s, b, ks); break;
-        }
-        if (e != cudaSuccess)
-            return e;
-    }
-    return cudaSuccess;
+    const int per_block = kRowsWarps / ks;
+    const int grid = static_cast<int>((groups + per_block - 1) / per_block);
+    if (a.T == 1)
+        return launch_pdl(int8_rows_kernel<T, 0>, grid, 32 * kRowsWarps, 0, s, a, ks);
+    if (a.T <= 8)
+        return launch_pdl(int8_rows_kernel<T, 1>, grid, 32 * kRowsWarps, 0, s, a, ks);
+    return launch_pdl(int8_rows_kernel<T, 2>, grid, 32 * kRowsWarps, 0, s, a, ks);
 }
 
 template <typename T, bool SILU>
