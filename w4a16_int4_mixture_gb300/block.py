@@ -13,6 +13,7 @@ contiguous):
 
 from __future__ import annotations
 
+import functools
 from typing import Optional
 
 import torch
@@ -83,7 +84,9 @@ def _codes(t, name: str, dev=None, shape=None) -> int:
 
 
 def _vec(t, name: str, dev, n: int):
-    ops._req(t, name, _F32, dev, 1)
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.device != dev or \
+            t.dim() != 1 or not t.is_contiguous():
+        ops._req(t, name, _F32, dev, 1)
     if t.numel() != n:
         raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
 
@@ -92,9 +95,27 @@ def _residual(t, dev, dtype, shape) -> int:
     return 0 if t is None else _rows(t, "residual", (dtype,), dev, shape)
 
 
-def _workspace(ws, dev, need: int):
-    # (allocated on the current stream, so that calls on several streams do not share it)
-    return torch.empty(need, dtype=torch.uint8, device=dev) if ws is None else ws
+_spaces = {}
+
+
+def _workspace(ws, dev, need: int, stream: int):
+    """The caller's workspace, or a buffer kept for each stream and grown on demand (an allocation
+    costs a call of one token a fifth of its host time).  Calls on one stream run in order, so
+    they share it; a captured graph, which may be replayed on any stream, gets its own."""
+    if ws is not None:
+        return ws
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    key = (dev.index, stream)
+    ws = _spaces.get(key)
+    if ws is None or ws.numel() < need:
+        ws = _spaces[key] = torch.empty(need, dtype=torch.uint8, device=dev)
+    return ws
+
+
+@functools.lru_cache(maxsize=4096)
+def _size(fn: str, *sizes: int) -> int:
+    return int(getattr(_C, fn)(*sizes))
 
 
 def moe_route(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = None,
@@ -121,9 +142,9 @@ def moe_route(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = None,
         ids, weights = out
         _pairs(ids, weights, dev, T, k)
     st = _C.chord_moe_route(_ptr(logits), _TYPES[logits.dtype], T, E, ld, k,
-                                   _SCORES[scoring], _ptr(bias), n_group, topk_group, group_top,
-                                   1 if renormalize else 0, scale, _ptr(ids), _ptr(weights),
-                                   _stream(dev))
+                            _SCORES[scoring], _ptr(bias), n_group, topk_group, group_top,
+                            1 if renormalize else 0, scale, _ptr(ids), _ptr(weights),
+                            _stream(dev))
     B.check(st, "chord_moe_route")
     return ids, weights
 
@@ -157,9 +178,9 @@ def moe_route_backward(d_weights: torch.Tensor, logits: torch.Tensor, topk_ids: 
         if tuple(out.shape) != (T, E):
             raise ValueError(f"out must be [{T}, {E}]")
     st = _C.chord_moe_route_backward(_ptr(d_weights), _ptr(logits), _TYPES[logits.dtype],
-                                            T, E, ld, k, _SCORES[scoring], 1 if renormalize else 0,
-                                            scale, _ptr(topk_ids), _ptr(topk_weights),
-                                            _ptr(out), _stream(dev))
+                                     T, E, ld, k, _SCORES[scoring], 1 if renormalize else 0,
+                                     scale, _ptr(topk_ids), _ptr(topk_weights),
+                                     _ptr(out), _stream(dev))
     B.check(st, "chord_moe_route_backward")
     return out
 
@@ -183,7 +204,7 @@ def _quantize(x, K: int, ld: int, out, fn: str):
         _vec(scale, "scale", dev, T)
     ld_q = _codes(q, "codes", dev, (T, K))
     st = getattr(_C, fn)(_ptr(x), _TYPES[x.dtype], T, K, ld, _ptr(q), ld_q,
-                                _ptr(scale), _stream(dev))
+                         _ptr(scale), _stream(dev))
     B.check(st, fn)
     return q, scale
 
@@ -231,18 +252,19 @@ def int8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale
     _vec(w_scale, "w_scale", dev, N)
     ld_r = _residual(residual, dev, out_dtype, (T, N))
     out, ld_out = _output(out, dev, out_dtype, (T, N))
-    ws = _workspace(workspace, dev, _C.chord_int8_matmul_workspace_size(T, K))
-    st = _C.chord_int8_matmul(_ptr(a), ld_a, _ptr(a_scale), _ptr(w), ld_w,
-                                     _ptr(w_scale), T, N, K, _ptr(residual), ld_r, _ptr(out),
-                                     _TYPES[out_dtype], ld_out, _ptr(ws), ws.numel(), flags,
-                                     _stream(dev))
-    B.check(st, "chord_int8_matmul")
+    st = _stream(dev)
+    ws = _workspace(workspace, dev, _size("chord_int8_matmul_workspace_size", T, K), st)
+    rc = _C.chord_int8_matmul(_ptr(a), ld_a, _ptr(a_scale), _ptr(w), ld_w,
+                              _ptr(w_scale), T, N, K, _ptr(residual), ld_r, _ptr(out),
+                              _TYPES[out_dtype], ld_out, _ptr(ws), ws.numel(), flags,
+                              st)
+    B.check(rc, "chord_int8_matmul")
     return out
 
 
 def int8_workspace_size(T: int, K: int, I: int = 0) -> int:
     """Workspace bytes of int8_linear (T, K) and of int8_mlp (T, H, I)."""
-    return int(_C.chord_int8_workspace_size(T, K, I))
+    return _size("chord_int8_workspace_size", T, K, I)
 
 
 def int8_linear(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
@@ -259,11 +281,12 @@ def int8_linear(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
     _vec(w_scale, "w_scale", dev, N)
     ld_r = _residual(residual, dev, x.dtype, (T, N))
     out, ld_out = _output(out, dev, x.dtype, (T, N))
-    ws = _workspace(workspace, dev, int8_workspace_size(T, K))
-    st = _C.chord_int8_linear(_ptr(x), _TYPES[x.dtype], ld_x, _ptr(w), ld_w,
-                                     _ptr(w_scale), T, N, K, _ptr(residual), ld_r, _ptr(out),
-                                     ld_out, _ptr(ws), ws.numel(), flags, _stream(dev))
-    B.check(st, "chord_int8_linear")
+    st = _stream(dev)
+    ws = _workspace(workspace, dev, int8_workspace_size(T, K), st)
+    rc = _C.chord_int8_linear(_ptr(x), _TYPES[x.dtype], ld_x, _ptr(w), ld_w,
+                              _ptr(w_scale), T, N, K, _ptr(residual), ld_r, _ptr(out),
+                              ld_out, _ptr(ws), ws.numel(), flags, st)
+    B.check(rc, "chord_int8_linear")
     return out
 
 
@@ -287,12 +310,13 @@ def int8_mlp(x: torch.Tensor, w13: torch.Tensor, w13_scale: torch.Tensor, w2: to
     _vec(w2_scale, "w2_scale", dev, H)
     ld_r = _residual(residual, dev, x.dtype, (T, H))
     out, ld_out = _output(out, dev, x.dtype, (T, H))
-    ws = _workspace(workspace, dev, int8_workspace_size(T, H, I))
-    st = _C.chord_int8_mlp(_ptr(x), _TYPES[x.dtype], ld_x, _ptr(w13), ld13,
-                                  _ptr(w13_scale), _ptr(w2), ld2, _ptr(w2_scale), T, H, I,
-                                  _ptr(residual), ld_r, _ptr(out), ld_out, _ptr(ws),
-                                  ws.numel(), flags, _stream(dev))
-    B.check(st, "chord_int8_mlp")
+    st = _stream(dev)
+    ws = _workspace(workspace, dev, int8_workspace_size(T, H, I), st)
+    rc = _C.chord_int8_mlp(_ptr(x), _TYPES[x.dtype], ld_x, _ptr(w13), ld13,
+                           _ptr(w13_scale), _ptr(w2), ld2, _ptr(w2_scale), T, H, I,
+                           _ptr(residual), ld_r, _ptr(out), ld_out, _ptr(ws),
+                           ws.numel(), flags, st)
+    B.check(rc, "chord_int8_mlp")
     return out
 
 

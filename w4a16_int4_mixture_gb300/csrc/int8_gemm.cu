@@ -82,7 +82,8 @@ struct Int8Cfg {
     static constexpr int OFF_BARS = OFF_B + AS * B_ITEM;
     static constexpr int NBARS = 2 * RS + 3 * AS + 4 + 1;
     static constexpr int OFF_MISC = OFF_BARS + 8 * NBARS;
-    static constexpr int SMEM = OFF_MISC + 16 + 1024;  // + alignment slack
+    static constexpr int OFF_AS = OFF_MISC + 16;  // token scales, a part for each epilogue warp
+    static constexpr int SMEM = OFF_AS + kEpiWarps * (NTMAX / 2) * 4 + 1024;  // + alignment slack
     static constexpr int A_COLS = HV * kHalfK / 2;
     static constexpr int D_COL0 = AS * A_COLS;
     static constexpr int TMEM_COLS = 512;
@@ -272,49 +273,57 @@ __device__ __forceinline__ void store_quad(const Int8Args& a, int64_t t, int n, 
             static_cast<T*>(a.out)[t * a.ld_out + n + i] = from_f32<T>(v[i]);
 }
 
-// out of one channel and 8 * NB tokens from t0 on (those below T, at most cols).
-// The loads of a batch of 8 go out before the stores of the batch before it,
-// which may write the residual: one at a time, each token waited for its own.
+// out of one channel and kBatch * NB tokens from t0 on (those below T, at most
+// cols); as: their scales in shared memory, zeros past T.  The residual's loads of a
+// batch go out before the stores of the batch before it, which may write the
+// residual: one at a time, each token waited for its own.
+constexpr int kBatch = 8;
 template <typename T, int NB>
-__device__ __forceinline__ void store_sums(const Int8Args& a, int64_t t0, int cols, int n, const int* sum, float ws)
+__device__ __forceinline__ void store_sums(const Int8Args& a, int64_t t0, int cols, int n, const int* sum,
+                                           const float* as, float ws)
 {
     const int lim = a.T - t0 < cols ? static_cast<int>(a.T - t0) : cols;
     const T* res = static_cast<const T*>(a.residual) + t0 * a.ld_r + n;
     T* out = static_cast<T*>(a.out) + t0 * a.ld_out + n;
-    const float* as = a.a_scale + t0;
-    T r[2][8];
+    T r[2][kBatch];
     auto load = [&](int b) {
+        if (kBatch * (b + 1) <= lim) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (8 * b + i < lim)
-                r[b & 1][i] = res[(8 * b + i) * a.ld_r];
+            for (int i = 0; i < kBatch; ++i)
+                r[b & 1][i] = res[(kBatch * b + i) * a.ld_r];
+        } else {
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                if (kBatch * b + i < lim)
+                    r[b & 1][i] = res[(kBatch * b + i) * a.ld_r];
+        }
     };
     if (a.residual)
         load(0);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-        if (8 * b < lim) {
-            float v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (8 * b + i < lim)
-                    v[i] = as[8 * b + i];
+        if (kBatch * b < lim) {
             if (a.residual && b + 1 < NB)
                 load(b + 1);
+            float v[kBatch];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (8 * b + i < lim)
-                    v[i] = static_cast<float>(sum[8 * b + i]) * v[i] * ws;
+            for (int i = 0; i < kBatch; ++i)
+                v[i] = static_cast<float>(sum[kBatch * b + i]) * as[kBatch * b + i] * ws;
             if (a.residual) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (8 * b + i < lim)
-                        v[i] += to_f32<T>(r[b & 1][i]);
+                for (int i = 0; i < kBatch; ++i)
+                    v[i] += to_f32<T>(r[b & 1][i]);
             }
+            if (kBatch * (b + 1) <= lim) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (8 * b + i < lim)
-                    out[(8 * b + i) * a.ld_out] = from_f32<T>(v[i]);
+                for (int i = 0; i < kBatch; ++i)
+                    out[(kBatch * b + i) * a.ld_out] = from_f32<T>(v[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i)
+                    if (kBatch * b + i < lim)
+                        out[(kBatch * b + i) * a.ld_out] = from_f32<T>(v[i]);
+            }
         }
     }
 }
@@ -544,12 +553,23 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const uint32_t tlane = static_cast<uint32_t>(q * 32) << 16;
         const int ncol = nt / 2, col0 = half * ncol;  // (nt % 16 == 0: ncol % 8 == 0)
         pdl_wait();  // (a_scale, residual)
+        float* as = reinterpret_cast<float*>(smem + C::OFF_AS) + (warp - C::EPI_WARP0) * (C::NTMAX / 2);
         int pc = 0;
         bool ok = true;
         for (int u = u0; u < g.units && ok; u += ustep) {
             int sum[C::NTMAX / 2];
             const int n = u % g.n_tiles * (kTileM * C::CG) + (C::CG == 2 ? rank * kTileM : 0) + q * 32 + lane;
             const int64_t t0 = static_cast<int64_t>(u / g.n_tiles) * nt + col0;
+            if (g.split == 1) {
+                // the tokens' scales, a copy for each warp
+#pragma unroll
+                for (int i = 0; i < (C::NTMAX / 2 + 31) / 32; ++i)
+                    if (32 * i + lane < C::NTMAX / 2)
+                        as[32 * i + lane] = 32 * i + lane < ncol && t0 + 32 * i + lane < g.p.T
+                                                ? g.p.a_scale[t0 + 32 * i + lane]
+                                                : 0.f;
+                __syncwarp();
+            }
             if (g.p.residual && g.split == 1) {
                 // the tile's residual comes into L2 while the unit is computed, a share
                 // of its 128-byte lines by each warp (rows may start inside a line)
@@ -600,7 +620,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         part[(col0 + j) * kTileM + q * 32 + lane] = sum[j];
             } else {
                 if (n < g.p.N)
-                    store_sums<T, C::NTMAX / 16>(g.p, t0, ncol, n, sum, g.p.w_scale[n]);
+                    store_sums<T, C::NTMAX / 2 / kBatch>(g.p, t0, ncol, n, sum, as, g.p.w_scale[n]);
             }
         }
     }
