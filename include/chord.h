@@ -486,7 +486,8 @@ chord_status chord_moe_route_backward(const float* d_weights, const void* logits
  *   q           device int8 [T, K], 16-byte aligned, rows ld_q bytes apart,
  *               ld_q % 16 == 0 (bytes past K are not written)
  *   scale       device float [T]
- * Limits: 1 <= K <= 131071 (CHORD_ERR_UNSUPPORTED_SHAPE).  T = 0 is allowed.
+ * Limits: 1 <= K <= 131071, T < 2^31 - 1024 (CHORD_ERR_UNSUPPORTED_SHAPE).  T = 0
+ *   is allowed.
  */
 chord_status chord_int8_quantize(const void* x, int type, int64_t T, int K, int64_t ld_x, int8_t* q,
                                  int64_t ld_q, float* scale, void* stream);
@@ -510,7 +511,7 @@ chord_status chord_int8_silu_mul_quantize(const void* gate_up, int type, int64_t
  *   workspace device, >= chord_int8_matmul_workspace_size(T, K) bytes,
  *             256-aligned (the device error word, and the tokens as fp16 codes)
  *   flags     0 or CHORD_FLAG_VALIDATE
- * Limits: 1 <= K <= 131071, N >= 1.  T = 0 is allowed.
+ * Limits: 1 <= K <= 131071, 1 <= N < 2^30, T < 2^31 - 1024.  T = 0 is allowed.
  *
  * chord_int8_linear: x [T, K] of `type` quantised per token, then the product.
  * chord_int8_mlp: a gated MLP (a shared expert) in 8-bit integers:

@@ -458,6 +458,31 @@ def test_linear_and_mlp_are_their_parts(chord, T, H, I, dt):
     assert ((want.double() - y64).norm() / y64.norm()).item() <= 0.05
 
 
+def test_offsets_past_32_bits(chord):
+    """More than 2^32 elements in an operand or an output: the last rows are right."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    T, N, K = 140000, 32768, 64
+    a, w = codes(T, K, g), codes(N, K, g)
+    sa, sw = torch.rand(T, device=DEV, generator=g) / 4096, torch.rand(N, device=DEV, generator=g)
+    y = chord.int8_matmul(a, sa, w, sw)
+    for rows in (slice(0, 3), slice(T - 5, T)):
+        want = torch.from_numpy(scaled_ref(product_ref(a[rows], w), sa[rows], sw)).bfloat16()
+        assert torch.equal(y[rows].cpu(), want)
+    del y
+    x = torch.zeros((1 << 22) + 9, 1024, dtype=torch.bfloat16, device=DEV)
+    x[-3:] = torch.randn(3, 1024, device=DEV, generator=g).bfloat16()
+    q, s = chord.int8_quantize(x)
+    rq, rs = quantize_ref(x[-3:].float().cpu().numpy())
+    assert np.array_equal(q[-3:].cpu().numpy(), rq) and np.array_equal(s[-3:].cpu().numpy(), rs)
+    ids, w = chord.moe_route(x, 8, scoring="sigmoid")
+    ids3, w3 = chord.moe_route(x[-3:].clone(), 8, scoring="sigmoid")
+    assert torch.equal(ids[-3:], ids3) and torch.equal(w[-3:], w3)
+    d = chord.moe_route_backward(torch.ones_like(w), x, ids, w, scoring="softmax", renormalize=False)
+    d3 = chord.moe_route_backward(torch.ones_like(w3), x[-3:].clone(), ids3, w3, scoring="softmax",
+                                  renormalize=False)
+    assert torch.equal(d[-3:], d3)
+
+
 def test_empty_batches(chord):
     w, s = chord.int8_quantize(torch.randn(48, 32, device=DEV))
     x = torch.zeros(0, 32, device=DEV)

@@ -27,11 +27,11 @@ chord_status check_ws(void* ws, size_t bytes, size_t need)
     return CHORD_OK;
 }
 
-// Sizes of a product of T tokens: every index below fits 63 bits and every
-// launch its grid.
+// Sizes of a product of T tokens: row numbers, rounded up to whole tiles, fit 32
+// bits (offsets are taken in 64).
 bool sizes_ok(int64_t T, int64_t N, int64_t K)
 {
-    return T < (int64_t(1) << 31) && N >= 1 && N < (int64_t(1) << 30) && K >= 1 && K <= kMaxK;
+    return T < (int64_t(1) << 31) - 1024 && N >= 1 && N < (int64_t(1) << 30) && K >= 1 && K <= kMaxK;
 }
 
 chord_status finish(int flags, void* ws, cudaStream_t s)

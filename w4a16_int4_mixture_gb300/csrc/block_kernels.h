@@ -94,8 +94,10 @@ struct Int8Args {
 // 8-bit codes [T, K], rows ld_a apart, as fp16, rows ld_out apart (multiples of 16)
 cudaError_t launch_int8_to_f16(const int8_t* a, int64_t ld_a, int64_t T, int K, __half* out, int64_t ld_out,
                                int* err, int sms, cudaStream_t s);
-// Up to this many tokens launch_int8_rows is taken.  (Measured with N = 4096, K =
-// 7168, both: 8 tokens %R8, 16 tokens %R16, us a product.)
+// Up to this many tokens launch_int8_rows is taken.  (Both measured, us a
+// product with N = 4096: 16 tokens, K = 7168 10.3 / 10.5, K = 2048 4.3 / 7.5; 9
+// tokens, K = 7168 9.9 / 10.5; 32 tokens, which it would take two more MMAs a step
+// for, 10.9 by launch_int8_gemm.)
 constexpr int64_t kInt8RowsMaxT = 16;
 // few tokens: mma.sync on the 8-bit codes (T <= kInt8RowsMaxT)
 cudaError_t launch_int8_rows(const Int8Args& a, int sms, cudaStream_t s);

@@ -231,7 +231,8 @@ __global__ void __launch_bounds__(256)
 // shared memory.  Both have low rates on this part (dp4a about 8 lanes a clock and
 // SM, mma.sync on 8-bit integers about 120 TOP/s, on fp16 about 215 TFLOP/s), and
 // this is the best of them for each count: K = 7168, N = 4096, us, weights in L2:
-// %TABLE
+//   1 token: dp4a 4.3, mma.sync 5.5;  8: dp4a 24.6, mma.sync on integers 6.3, on
+//   fp16 7.3;  16: on integers 10.3, on fp16 9 to 12 (its codes converted here)
 constexpr int kRowsM = 16;     // channels of a warp (the MMA's M)
 constexpr int kRowsWarps = 16;  // warps of a block: parts of K, or channel groups
 constexpr int kRowsK = 64;     // codes of a step: two MMAs of K = 32
