@@ -64,16 +64,20 @@ struct Int8Gemm {
 };
 
 // CG CTAs per tile, token tile, raw weight stages, halves of 64 codes per item,
-// items in flight (weights in tensor memory, tokens in shared memory: one ring),
-// converter groups, and the registers of a producer / converter / epilogue
-// thread (0: as launched)
-template <int CG_, int NTMAX_, int RS_, int HV_, int AS_, int NG_, int R0_ = 0, int RC_ = 0, int RE_ = 0>
+// token items in shared memory, weight items in tensor memory, converter groups,
+// and the registers of a producer / converter / epilogue thread (0: as launched).
+// BS > AS: a token item is under way before the weight item that it meets has a
+// place, for which tiles below 160 wait otherwise; BS = AS: one ring and one commit
+// an item instead of two, which the issuer of 64-code items needs more.
+template <int CG_, int NTMAX_, int RS_, int HV_, int BS_, int AS_, int NG_, int R0_ = 0, int RC_ = 0, int RE_ = 0>
 struct Int8Cfg {
     static constexpr int CG = CG_;
     static constexpr int NTMAX = NTMAX_;
     static constexpr int RS = RS_;
     static constexpr int HV = HV_;
+    static constexpr int BS = BS_;
     static constexpr int AS = AS_;
+    static constexpr bool ONE_RING = BS == AS;  // a token item is released with its weight item
     static constexpr int CHAIN = kChainK / (kHalfK * HV);  // items of a chain
     static constexpr int NG = NG_;
     static constexpr int R0 = R0_, RC = RC_, RE = RE_;
@@ -85,8 +89,8 @@ struct Int8Cfg {
     static constexpr int B_ITEM = HV * B_HALF;
     static constexpr int OFF_W = 0;
     static constexpr int OFF_B = OFF_W + RS * W_RAW;
-    static constexpr int OFF_BARS = OFF_B + AS * B_ITEM;
-    static constexpr int NBARS = 2 * RS + 3 * AS + 4 + 1;
+    static constexpr int OFF_BARS = OFF_B + BS * B_ITEM;
+    static constexpr int NBARS = 2 * RS + 2 * BS + 2 * AS + 4 + 1;
     static constexpr int OFF_MISC = OFF_BARS + 8 * NBARS;
     static constexpr int OFF_AS = OFF_MISC + 16;  // token scales, a part for each epilogue warp
     static constexpr int SMEM = OFF_AS + kEpiWarps * (NTMAX / 2) * 4 + 1024;  // + alignment slack
@@ -262,21 +266,78 @@ __device__ __forceinline__ int4 ld_cluster_s32x4(uint32_t addr, uint32_t rank)
 
 // out of one token and four channels from n on (those below N)
 template <typename T>
-__device__ __forceinline__ void store_quad(const Int8Args& a, int64_t t, int n, const int (&sum)[4])
+__device__ __forceinline__ void store_quad(const Int8Args& a, int64_t t, int n, const int (&sum)[4], float as,
+                                           const float (&ws)[4])
 {
-    const float as = a.a_scale[t];
+    struct alignas(4 * sizeof(T)) Quad {
+        T e[4];
+    };
     float v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        if (n + i < a.N) {
-            v[i] = static_cast<float>(sum[i]) * as * a.w_scale[n + i];
-            if (a.residual)
+        v[i] = static_cast<float>(sum[i]) * as * ws[i];
+    if (a.residual) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (n + i < a.N)
                 v[i] += to_f32<T>(static_cast<const T*>(a.residual)[t * a.ld_r + n + i]);
-        }
+    }
+    Quad q;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        if (n + i < a.N)
-            static_cast<T*>(a.out)[t * a.ld_out + n + i] = from_f32<T>(v[i]);
+        q.e[i] = from_f32<T>(v[i]);
+    T* out = static_cast<T*>(a.out) + t * a.ld_out + n;
+    if (n + 4 <= a.N && reinterpret_cast<uintptr_t>(out) % sizeof(Quad) == 0) {
+        *reinterpret_cast<Quad*>(out) = q;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (n + i < a.N)
+                out[i] = q.e[i];
+    }
+}
+
+// Split K: adds the S parts' sums of columns c0, c0 + kJoinStep ... below c1 and
+// stores them, four channels of a column at a time.  Several columns at once, so
+// that eight loads from other CTAs' shared memory and all that is read from memory
+// are in flight together: one at a time, and on the few registers that a
+// producer's thread is left, the join took 6 of 30 us at 300 tokens, K = 7168, two
+// parts.  at: this thread's channels of column 0 (shared memory address).
+constexpr int kJoinStep = kEpiWarps * 32 / (kTileM / 4);
+template <typename T, int CG, int S>
+__device__ __forceinline__ void join_parts(const Int8Args& a, uint32_t at, int rank, int c0, int c1, int64_t t0, int n,
+                                           const float (&ws)[4])
+{
+    constexpr int kCols = kMaxSplit / S;
+    for (int col = c0; col < c1; col += kCols * kJoinStep) {
+        float as[kCols];
+        int4 v[kCols][S];
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) {
+            const int c = col + j * kJoinStep;
+            const bool real = c < c1 && t0 + c < a.T;
+            as[j] = real ? a.a_scale[t0 + c] : 0.f;
+            if (real)
+#pragma unroll
+                for (int k = 0; k < S; ++k)
+                    v[j][k] = ld_cluster_s32x4(at + 4u * kTileM * c, k * CG + rank);
+        }
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) {
+            const int c = col + j * kJoinStep;
+            if (c < c1 && t0 + c < a.T) {
+                int sum[4] = {};
+#pragma unroll
+                for (int k = 0; k < S; ++k) {
+                    sum[0] += v[j][k].x;
+                    sum[1] += v[j][k].y;
+                    sum[2] += v[j][k].z;
+                    sum[3] += v[j][k].w;
+                }
+                store_quad<T>(a, t0 + c, n, sum, as[j], ws);
+            }
+        }
+    }
 }
 
 // out of one channel and kBatch * NB tokens from t0 on (those below T, at most
@@ -355,10 +416,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     auto raw_full = [&](int s) { return bar0 + 8u * s; };
     auto raw_empty = [&](int s) { return bar0 + 8u * (C::RS + s); };
     auto tok_full = [&](int s) { return bar0 + 8u * (2 * C::RS + s); };
-    auto cv_full = [&](int s) { return bar0 + 8u * (2 * C::RS + C::AS + s); };
-    auto cv_empty = [&](int s) { return bar0 + 8u * (2 * C::RS + 2 * C::AS + s); };
-    auto acc_full = [&](int s) { return bar0 + 8u * (2 * C::RS + 3 * C::AS + s); };
-    auto acc_empty = [&](int s) { return bar0 + 8u * (2 * C::RS + 3 * C::AS + 2 + s); };
+    auto tok_empty = [&](int s) { return bar0 + 8u * (2 * C::RS + C::BS + s); };
+    auto cv_full = [&](int s) { return bar0 + 8u * (2 * C::RS + 2 * C::BS + s); };
+    auto cv_empty = [&](int s) { return bar0 + 8u * (2 * C::RS + 2 * C::BS + C::AS + s); };
+    auto acc_full = [&](int s) { return bar0 + 8u * (2 * C::RS + 2 * C::BS + 2 * C::AS + s); };
+    auto acc_empty = [&](int s) { return bar0 + 8u * (2 * C::RS + 2 * C::BS + 2 * C::AS + 2 + s); };
     const uint32_t drain_bar = bar0 + 8u * (C::NBARS - 1);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
@@ -369,8 +431,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             mbar_init(raw_full(s), 1);
             mbar_init(raw_empty(s), 8);  // (four warps for each half)
         }
-        for (int s = 0; s < C::AS; ++s) {
+        for (int s = 0; s < C::BS; ++s) {
             mbar_init(tok_full(s), 1);
+            mbar_init(tok_empty(s), 1);
+        }
+        for (int s = 0; s < C::AS; ++s) {
             mbar_init(cv_full(s), 4 * C::HV * C::CG);
             mbar_init(cv_empty(s), 1);
         }
@@ -440,8 +505,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 const int row = u / g.n_tiles * nt + row0;
                 int k = k0 * kRawK;
                 for (int c = 0; c < unit_items; ++c, ++j) {
-                    const int s = j % C::AS;
-                    if (!mbar_wait(cv_empty(s), ((j / C::AS) & 1) ^ 1, abort_flag, err)) {
+                    const int s = j % C::BS;
+                    if (!mbar_wait(C::ONE_RING ? cv_empty(s) : tok_empty(s), ((j / C::BS) & 1) ^ 1, abort_flag,
+                                   err)) {
                         ok = false;
                         break;
                     }
@@ -461,7 +527,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             // ------------------------------------------------------- MMA issuer
             const uint32_t idesc = idesc_f16_f32(kTileM * C::CG, nt);
             const uint64_t bdesc0 = smem_desc_sw128(sbase + C::OFF_B);
-            int s = 0, pc = 0, any = 0;
+            int s = 0, b = 0, pc = 0, any = 0;
             uint32_t phase = 0;
             bool ok = true;
             for (int u = 0; u < my_units && ok; ++u) {
@@ -480,10 +546,15 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                             break;
                         }
                         tc_fence_after();
-                        mma_item<C::CG, C::HV, C::B_HALF / 16>(d, tmem + s * C::A_COLS, bdesc0 + s * (C::B_ITEM / 16),
+                        mma_item<C::CG, C::HV, C::B_HALF / 16>(d, tmem + s * C::A_COLS, bdesc0 + (C::ONE_RING ? s : b) * (C::B_ITEM / 16),
                                                         idesc, c != c0 ? 1u : 0u);
                         any = 1;
                         commit_elect<C::CG>(cv_empty(s), pair);
+                        if constexpr (!C::ONE_RING) {
+                            commit_elect<C::CG>(tok_empty(b), pair);
+                            if (++b == C::BS)
+                                b = 0;
+                        }
                         if (++s == C::AS) {
                             s = 0;
                             phase ^= 1u;
@@ -498,6 +569,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 mbar_drain(drain_bar, 0);
             }
             __syncwarp();
+        }
+        if (g.split > 1) {  // (the partial sums: see the epilogue)
+            __syncwarp();
+            cluster_sync_all();
         }
     } else if (warp < C::EPI_WARP0) {
         // ------------------------------------------------------------ converters
@@ -534,7 +609,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             if (lane == 0)
                 mbar_arrive(raw_empty(rs));
             // (the arrival below also stands for this CTA's tokens of the item)
-            if (!mbar_wait(tok_full(s), (it / C::AS) & 1, abort_flag, err) ||
+            if (!mbar_wait(tok_full(it % C::BS), (it / C::BS) & 1, abort_flag, err) ||
                 !mbar_wait(cv_empty(s), ((it / C::AS) & 1) ^ 1, abort_flag, err)) {
                 ok = false;
                 break;
@@ -550,7 +625,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         // (pair: the last arrivals from the first CTA's commits have landed)
         if (C::CG == 2 && ok && j > grp) {
             const int it = (j - C::NG) / C::HV;
-            mbar_wait(cv_empty(it % C::AS), (it / C::AS) & 1, abort_flag, err);
+            if (mbar_wait(cv_empty(it % C::AS), (it / C::AS) & 1, abort_flag, err) && !C::ONE_RING)
+                mbar_wait(tok_empty(it % C::BS), (it / C::BS) & 1, abort_flag, err);
+        }
+        if (g.split > 1) {
+            __syncwarp();
+            cluster_sync_all();
         }
     } else {
         // -------------------------------------------------------------- epilogue
@@ -626,52 +706,46 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     store_sums<T, C::NTMAX / 2 / kBatch>(g.p, t0, ncol, n, sum, as, g.p.w_scale[n]);
             }
         }
+        if (g.split > 1) {
+            // every CTA of the cluster finishes a share of its token columns
+            const int et = threadIdx.x - C::EPI_WARP0 * 32, r = et % (kTileM / 4) * 4;
+            const int n = u0 % g.n_tiles * (kTileM * C::CG) + rank * kTileM + r;
+            const int64_t t0 = static_cast<int64_t>(u0 / g.n_tiles) * nt;
+            const int c1 = (krank + 1) * nt / g.split;
+            float ws[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                ws[i] = n + i < g.p.N ? g.p.w_scale[n + i] : 0.f;
+            __syncwarp();
+            cluster_sync_all();
+            const int c0 = krank * nt / g.split + et / (kTileM / 4);
+            const uint32_t at = sbase + 4u * r;
+            if (g.split == 2)
+                join_parts<T, C::CG, 2>(g.p, at, rank, c0, c1, t0, n, ws);
+            else if (g.split == 4)
+                join_parts<T, C::CG, 4>(g.p, at, rank, c0, c1, t0, n, ws);
+            else
+                join_parts<T, C::CG, 8>(g.p, at, rank, c0, c1, t0, n, ws);
+        }
     }
 
     tc_fence_before();
     __syncthreads();
     if (*abort_flag && (warp == 0 || warp == 3)) {
         // copies issued but never consumed land before the CTA ends
-        const int depth = warp == 0 ? C::RS : C::AS;
+        const int depth = warp == 0 ? C::RS : C::BS;
         if (lane == 0)
             for (int i = issued > depth ? issued - depth : 0; i < issued; ++i)
-                mbar_drain(warp == 0 ? raw_full(i % C::RS) : tok_full(i % C::AS), (i / depth) & 1);
+                mbar_drain(warp == 0 ? raw_full(i % C::RS) : tok_full(i % C::BS), (i / depth) & 1);
         __syncwarp();
     }
-    if constexpr (C::CG == 2)
-        cluster_sync_all();  // (neither CTA frees what the other's MMAs still use)
+    // neither CTA of a pair frees what the other's MMAs still use, and partial sums
+    // stay until every CTA has read them
+    if (C::CG == 2 || g.split > 1)
+        cluster_sync_all();
     if (warp == 2) {
         tc_fence_after();
         tmem_dealloc_cg<C::CG>(tmem, C::TMEM_COLS);
-    }
-    if (g.split > 1) {
-        // every CTA of the cluster finishes a share of its token columns, four
-        // channels a thread, the loads from all parts at once
-        __syncthreads();
-        cluster_sync_all();
-        pdl_wait();
-        const int n0 = u0 % g.n_tiles * (kTileM * C::CG) + rank * kTileM;
-        const int64_t t0 = static_cast<int64_t>(u0 / g.n_tiles) * nt;
-        const int c0 = krank * nt / g.split, c1 = (krank + 1) * nt / g.split;
-        for (int i = threadIdx.x; i < (c1 - c0) * (kTileM / 4); i += C::THREADS) {
-            const int col = c0 + i / (kTileM / 4), r = i % (kTileM / 4) * 4;
-            const uint32_t at = sbase + 4u * (col * kTileM + r);
-            int4 v[kMaxSplit];
-#pragma unroll
-            for (int k = 0; k < kMaxSplit; ++k)
-                v[k] = k < g.split ? ld_cluster_s32x4(at, k * C::CG + rank) : make_int4(0, 0, 0, 0);
-            int sum[4] = {};
-#pragma unroll
-            for (int k = 0; k < kMaxSplit; ++k) {
-                sum[0] += v[k].x;
-                sum[1] += v[k].y;
-                sum[2] += v[k].z;
-                sum[3] += v[k].w;
-            }
-            if (t0 + col < g.p.T)
-                store_quad<T>(g.p, t0 + col, n0 + r, sum);
-        }
-        cluster_sync_all();  // (the partial sums stay until every CTA has read them)
     }
 }
 
@@ -751,25 +825,32 @@ cudaError_t launch_cfg(Int8Gemm g, int sms, cudaStream_t s)
 
 // 64-code items: more of them in flight in the same tensor memory, which the
 // round trip between the two CTAs of a pair needs; 128: fewer turns of the issuer,
-// for which a small tile is too short
-using CfgT32 = Int8Cfg<1, 32, 9, 2, 4, 4>;
-using CfgT128 = Int8Cfg<1, 128, 5, 2, 4, 3, 40, 64, 120>;
-using CfgP160 = Int8Cfg<2, 160, 8, 1, 6, 2, 40, 72, 144>;
+// for which a small tile is too short.  Measured, us with the conversion of 8-bit
+// codes: 8192 x 7168 x 4096 in tiles of 160 317 (two rings: 330;
+// tiles of 128: 342), 8192 x 2048 x 7168 in tiles of 192 157 (160: 173; 128:
+// 188), 512 x 7168 x 4096 in tiles of 128 31.5 (with two converter groups 34.4)
+using CfgT32 = Int8Cfg<1, 32, 8, 2, 8, 4, 4>;
+using CfgT128 = Int8Cfg<1, 128, 4, 2, 4, 4, 3, 40, 64, 120>;
+using CfgP128 = Int8Cfg<2, 128, 5, 2, 6, 4, 3, 40, 72, 112>;
+using CfgP160 = Int8Cfg<2, 160, 8, 1, 6, 6, 2, 40, 72, 144>;
+using CfgP192 = Int8Cfg<2, 192, 6, 1, 9, 4, 2, 32, 64, 160>;
 
-// Parts of K: doubled while the units' parts fit the SMs and each keeps at least
-// two raw stages.  Clusters of 8 only where they leave half of the SMs free: they
-// must find their SMs in one GPC each, and a GPC short of them costs a second
-// round (16 clusters of 8: 21 us where 32 of 4 took 13).
+// Clusters of one CTA per SM that run at once.  A cluster finds its SMs in one GPC,
+// so some stay free: cudaOccupancyMaxActiveClusters gives 76 of 2, 36 of 4 and 15
+// of 8 on 152 SMs (16 clusters of 8 took 21 us where 32 of 4 took 13).
+int cluster_seats(int cluster, int sms)
+{
+    return sms / cluster - (cluster == 8 ? 4 : cluster == 4 ? 2 : 0);
+}
+
+// Parts of K: doubled while the units' clusters run at once and each part keeps at
+// least two raw stages.
 int split_of(int64_t units, int cg, int K, int sms)
 {
     const int KT = (K + kRawK - 1) / kRawK;
     int split = 1;
-    while (KT >= 4 * split) {
-        const int64_t ctas = units * split * 2 * cg;
-        if (ctas > sms || split * 2 * cg > 8 || (split * 2 * cg == 8 && ctas > sms / 2))
-            break;
+    while (KT >= 4 * split && 2 * split * cg <= 8 && units <= cluster_seats(2 * split * cg, sms))
         split *= 2;
-    }
     return split;
 }
 
@@ -788,16 +869,17 @@ cudaError_t launch_type(const Int8Args& a, int sms, cudaStream_t s)
         return launch_cfg<CfgT128, T>(g, sms, s);
     }
     // CTA pairs (N of their MMA is a multiple of 32): the token tile for which the
-    // rounds of units cost least, in clocks as measured: an item takes its MMAs'
-    // 2 nt clocks and the handshakes between the CTAs, at least the converters'
-    // 430; a unit some 5000 more, and 8000 where its parts are joined
+    // rounds of units cost least, in clocks as measured: 64 codes take the MMAs' 2
+    // nt clocks and the handshakes between the CTAs, at least 390 of the converters
+    // (three groups, which leave registers for a tile of 128); a unit some 5000
+    // more, and 8000 where its parts are joined
     g.n_tiles = (a.N + 2 * kTileM - 1) / (2 * kTileM);
     const int64_t items = (a.K + kHalfK - 1) / kHalfK, pairs = sms / 2;
     int64_t best = INT64_MAX, units = 0;
-    for (int nt = CfgP160::NTMAX; nt >= 64; nt -= 32) {
+    for (int nt = CfgP192::NTMAX; nt >= 64; nt -= 32) {
         const int64_t u = (a.T + nt - 1) / nt * g.n_tiles;
         const int split = split_of(u, 2, a.K, sms);
-        const int64_t item = 2 * nt + 150 > 430 ? 2 * nt + 150 : 430;
+        const int64_t item = nt <= CfgP128::NTMAX ? 390 : 2 * nt + 110;
         const int64_t rounds = (u * split + pairs - 1) / pairs;
         const int64_t cost = rounds * (items / split * item + (split > 1 ? 13000 : 5000));
         if (cost < best) {
@@ -810,7 +892,11 @@ cudaError_t launch_type(const Int8Args& a, int sms, cudaStream_t s)
     if (units > INT32_MAX)
         return cudaErrorInvalidValue;
     g.units = static_cast<int>(units);
-    return launch_cfg<CfgP160, T>(g, sms, s);
+    if (g.nt <= CfgP128::NTMAX)
+        return launch_cfg<CfgP128, T>(g, sms, s);
+    if (g.nt <= CfgP160::NTMAX)
+        return launch_cfg<CfgP160, T>(g, sms, s);
+    return launch_cfg<CfgP192, T>(g, sms, s);
 }
 
 }  // namespace
