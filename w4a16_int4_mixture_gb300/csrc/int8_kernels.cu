@@ -144,11 +144,13 @@ __global__ void __launch_bounds__(1024) int8_quantize_kernel(QuantArgs a)
             a.scale[t] = scale;
         int8_t* q = a.q + t * a.ld_q;
         __half* q16 = a.q16 + t * a.ld_q;
-        auto store8 = [&](int k, const C& x) {
+        auto store8 = [&](int k, C& x) {
+            if (inv == 0.f)  // (the whole row: its values may be infinities or NaN)
+                x = C{};
             float r[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                r[i] = inv != 0.f ? __fadd_rn(__fmul_rn(x.v.at(i), inv), kRint) : kRint;
+                r[i] = __fadd_rn(__fmul_rn(x.v.at(i), inv), kRint);
             if (a.q16) {
                 __half2 h[4];
 #pragma unroll
