@@ -103,6 +103,7 @@ def _workspace(ws, dev, need: int, stream: int):
     costs a call of one token a fifth of its host time).  Calls on one stream run in order, so
     they share it; a captured graph, which may be replayed on any stream, gets its own."""
     if ws is not None:
+        ops._req(ws, "workspace", (torch.uint8,), dev, 1)
         return ws
     if torch.cuda.is_current_stream_capturing():
         return torch.empty(need, dtype=torch.uint8, device=dev)
@@ -141,9 +142,9 @@ def moe_route(logits: torch.Tensor, k: int, bias: Optional[torch.Tensor] = None,
     else:
         ids, weights = out
         _pairs(ids, weights, dev, T, k)
-    st = _C.chord_moe_route(_ptr(logits), _TYPES[logits.dtype], T, E, ld, k,
+    st = _C.chord_moe_route(logits.data_ptr(), _TYPES[logits.dtype], T, E, ld, k,
                             _SCORES[scoring], _ptr(bias), n_group, topk_group, group_top,
-                            1 if renormalize else 0, scale, _ptr(ids), _ptr(weights),
+                            1 if renormalize else 0, scale, ids.data_ptr(), weights.data_ptr(),
                             _stream(dev))
     B.check(st, "chord_moe_route")
     return ids, weights
@@ -177,10 +178,10 @@ def moe_route_backward(d_weights: torch.Tensor, logits: torch.Tensor, topk_ids: 
         ops._req(out, "out", (logits.dtype,), dev, 2)
         if tuple(out.shape) != (T, E):
             raise ValueError(f"out must be [{T}, {E}]")
-    st = _C.chord_moe_route_backward(_ptr(d_weights), _ptr(logits), _TYPES[logits.dtype],
+    st = _C.chord_moe_route_backward(d_weights.data_ptr(), logits.data_ptr(), _TYPES[logits.dtype],
                                      T, E, ld, k, _SCORES[scoring], 1 if renormalize else 0,
-                                     scale, _ptr(topk_ids), _ptr(topk_weights),
-                                     _ptr(out), _stream(dev))
+                                     scale, topk_ids.data_ptr(), topk_weights.data_ptr(),
+                                     out.data_ptr(), _stream(dev))
     B.check(st, "chord_moe_route_backward")
     return out
 
@@ -203,8 +204,8 @@ def _quantize(x, K: int, ld: int, out, fn: str):
         q, scale = out
         _vec(scale, "scale", dev, T)
     ld_q = _codes(q, "codes", dev, (T, K))
-    st = getattr(_C, fn)(_ptr(x), _TYPES[x.dtype], T, K, ld, _ptr(q), ld_q,
-                         _ptr(scale), _stream(dev))
+    st = getattr(_C, fn)(x.data_ptr(), _TYPES[x.dtype], T, K, ld, q.data_ptr(), ld_q,
+                         scale.data_ptr(), _stream(dev))
     B.check(st, fn)
     return q, scale
 
@@ -254,11 +255,12 @@ def int8_matmul(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale
     out, ld_out = _output(out, dev, out_dtype, (T, N))
     st = _stream(dev)
     ws = _workspace(workspace, dev, _size("chord_int8_matmul_workspace_size", T, K), st)
-    rc = _C.chord_int8_matmul(_ptr(a), ld_a, _ptr(a_scale), _ptr(w), ld_w,
-                              _ptr(w_scale), T, N, K, _ptr(residual), ld_r, _ptr(out),
-                              _TYPES[out_dtype], ld_out, _ptr(ws), ws.numel(), flags,
+    rc = _C.chord_int8_matmul(a.data_ptr(), ld_a, a_scale.data_ptr(), w.data_ptr(), ld_w,
+                              w_scale.data_ptr(), T, N, K, _ptr(residual), ld_r, out.data_ptr(),
+                              _TYPES[out_dtype], ld_out, ws.data_ptr(), ws.numel(), flags,
                               st)
-    B.check(rc, "chord_int8_matmul")
+    if rc:
+        B.check(rc, "chord_int8_matmul")
     return out
 
 
@@ -283,10 +285,11 @@ def int8_linear(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
     out, ld_out = _output(out, dev, x.dtype, (T, N))
     st = _stream(dev)
     ws = _workspace(workspace, dev, int8_workspace_size(T, K), st)
-    rc = _C.chord_int8_linear(_ptr(x), _TYPES[x.dtype], ld_x, _ptr(w), ld_w,
-                              _ptr(w_scale), T, N, K, _ptr(residual), ld_r, _ptr(out),
-                              ld_out, _ptr(ws), ws.numel(), flags, st)
-    B.check(rc, "chord_int8_linear")
+    rc = _C.chord_int8_linear(x.data_ptr(), _TYPES[x.dtype], ld_x, w.data_ptr(), ld_w,
+                              w_scale.data_ptr(), T, N, K, _ptr(residual), ld_r, out.data_ptr(),
+                              ld_out, ws.data_ptr(), ws.numel(), flags, st)
+    if rc:
+        B.check(rc, "chord_int8_linear")
     return out
 
 
@@ -312,11 +315,12 @@ def int8_mlp(x: torch.Tensor, w13: torch.Tensor, w13_scale: torch.Tensor, w2: to
     out, ld_out = _output(out, dev, x.dtype, (T, H))
     st = _stream(dev)
     ws = _workspace(workspace, dev, int8_workspace_size(T, H, I), st)
-    rc = _C.chord_int8_mlp(_ptr(x), _TYPES[x.dtype], ld_x, _ptr(w13), ld13,
-                           _ptr(w13_scale), _ptr(w2), ld2, _ptr(w2_scale), T, H, I,
-                           _ptr(residual), ld_r, _ptr(out), ld_out, _ptr(ws),
+    rc = _C.chord_int8_mlp(x.data_ptr(), _TYPES[x.dtype], ld_x, w13.data_ptr(), ld13,
+                           w13_scale.data_ptr(), w2.data_ptr(), ld2, w2_scale.data_ptr(), T, H, I,
+                           _ptr(residual), ld_r, out.data_ptr(), ld_out, ws.data_ptr(),
                            ws.numel(), flags, st)
-    B.check(rc, "chord_int8_mlp")
+    if rc:
+        B.check(rc, "chord_int8_mlp")
     return out
 
 

@@ -41,10 +41,6 @@ chord_status finish(int flags, void* ws, cudaStream_t s)
     return chord_get_device_error(ws, nullptr, 0, s);
 }
 
-// bytes of a token code between the kernels: 1, or 2 as the fp16 operand of
-// launch_int8_gemm
-int code_size(int64_t T) { return T <= kInt8RowsMaxT ? 1 : 2; }
-
 struct Scratch {  // of chord_int8_linear and chord_int8_mlp
     size_t codes, scales, mid, codes2, scales2, total;
 };
@@ -57,11 +53,11 @@ Scratch scratch(int64_t T, int K, int I)
         at += align_up(bytes);
         return r;
     };
-    p.codes = take(static_cast<size_t>(T) * pad16(K) * code_size(T));
+    p.codes = take(static_cast<size_t>(T) * pad16(K) * 2);  // (8-bit codes, or fp16)
     p.scales = take(static_cast<size_t>(T) * 4);
     if (I > 0) {
         p.mid = take(static_cast<size_t>(T) * 2 * I * 4);
-        p.codes2 = take(static_cast<size_t>(T) * pad16(I) * code_size(T));
+        p.codes2 = take(static_cast<size_t>(T) * pad16(I) * 2);
         p.scales2 = take(static_cast<size_t>(T) * 4);
     }
     p.total = at;
@@ -73,7 +69,7 @@ Scratch scratch(int64_t T, int K, int I)
 cudaError_t quantize_product(QuantArgs q, Int8Args g, void* codes, float* scales, const DeviceInfo& dev,
                              cudaStream_t s)
 {
-    const bool rows = g.T <= kInt8RowsMaxT;
+    const bool rows = takes_rows(g.T, g.N, g.K);
     q.q = rows ? static_cast<int8_t*>(codes) : nullptr;
     q.q16 = rows ? nullptr : static_cast<__half*>(codes);
     q.ld_q = g.ld_a = pad16(g.K);
@@ -190,7 +186,7 @@ size_t chord_int8_matmul_workspace_size(int64_t T, int K)
 {
     if (T < 0 || !sizes_ok(T, 1, K))
         return 0;
-    return kHeader + (T <= kInt8RowsMaxT ? 0 : align_up(static_cast<size_t>(T) * pad16(K) * 2));
+    return kHeader + (T <= 8 ? 0 : align_up(static_cast<size_t>(T) * pad16(K) * 2));
 }
 
 chord_status chord_int8_matmul(const int8_t* a, int64_t ld_a, const float* a_scale, const int8_t* w,
@@ -220,7 +216,7 @@ chord_status chord_int8_matmul(const int8_t* a, int64_t ld_a, const float* a_sca
     PdlScope pdl(T <= kPdlMaxRows);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
-    if (T <= kInt8RowsMaxT) {
+    if (takes_rows(T, N, K)) {
         e = launch_int8_rows(g, dev.sms, s);
     } else {
         __half* a16 = reinterpret_cast<__half*>(static_cast<uint8_t*>(workspace) + kHeader);

@@ -94,11 +94,16 @@ struct Int8Args {
 // 8-bit codes [T, K], rows ld_a apart, as fp16, rows ld_out apart (multiples of 16)
 cudaError_t launch_int8_to_f16(const int8_t* a, int64_t ld_a, int64_t T, int K, __half* out, int64_t ld_out,
                                int* err, int sms, cudaStream_t s);
-// Up to this many tokens launch_int8_rows is taken.  (Both measured, us a
-// product with N = 4096: 16 tokens, K = 7168 10.3 / 10.5, K = 2048 4.3 / 7.5; 9
-// tokens, K = 7168 9.9 / 10.5; 32 tokens, which it would take two more MMAs a step
-// for, 10.9 by launch_int8_gemm.)
+// Whether launch_int8_rows is taken: up to 8 tokens, up to 16 for weights of at most
+// 2^24 codes, where its MMAs' low rate costs less than the other's fixed time.  (Both
+// measured, us with the quantisation: 16 tokens, 7168 x 4096 from memory 14.4 / 12.4,
+// in L2 10.2 / 10.5 without it; 4096 x 4096 6.8 / 8.9, 2048 x 7168 6.8 / 8.8 without; 8
+// tokens, 7168 x 4096 10.5 / 12.4.)
 constexpr int64_t kInt8RowsMaxT = 16;
+inline bool takes_rows(int64_t T, int64_t N, int64_t K)
+{
+    return T <= 8 || (T <= kInt8RowsMaxT && N * K <= (int64_t(1) << 24));
+}
 // few tokens: mma.sync on the 8-bit codes (T <= kInt8RowsMaxT)
 cudaError_t launch_int8_rows(const Int8Args& a, int sms, cudaStream_t s);
 // more: tcgen05 on fp16 codes; a.after_codes must hold

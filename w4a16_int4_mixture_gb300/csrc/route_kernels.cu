@@ -23,7 +23,7 @@ constexpr uint32_t kKeyMasked = 0x007fffffu;
 __device__ __forceinline__ uint32_t order_key(float v)
 {
     const uint32_t u = __float_as_uint(v);
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+    return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float order_value(uint32_t k)
 {
@@ -168,13 +168,13 @@ __device__ void route_token(const MoeRouteArgs& a, int64_t t, int warp, int lane
             if (a.bias || groups) {
                 v = sigmoid ? sigmoid_f32(x[i]) : expf(x[i] - top);
                 if (a.bias) {
-                    v = (sigmoid ? v : v / sum) + bias.v[i] + 0.f;
-                    v = v == v ? v : -INFINITY;  // (a NaN bias masks its expert)
+                    v = (sigmoid ? v : v / sum) + bias.v[i];
                 }
                 if (groups)
-                    vals[e + i] = real ? v : -INFINITY;
+                    vals[e + i] = real && v > -INFINITY ? v : -INFINITY;
             }
-            k.v[i] = real ? order_key(a.bias ? v : x[i]) : kKeyMasked;
+            // (v > -inf: a NaN bias, which makes v NaN, masks its expert)
+            k.v[i] = real && (!a.bias || v > -INFINITY) ? order_key(a.bias ? v : x[i]) : kKeyMasked;
             if (!groups)
                 push(k.v[i], e + i);
         }
@@ -198,9 +198,10 @@ __device__ void route_token(const MoeRouteArgs& a, int64_t t, int warp, int lane
 #pragma unroll
                 for (int i = 0; i < Q; ++i) {
                     x[i] = clamp_logit(to_f32<TL>(raw[j].v[i]));
-                    m = fmaxf(m, x[i]);
-                    if (!sigmoid)
+                    if (!sigmoid) {
+                        m = fmaxf(m, x[i]);
                         keys[e0 + 32 * Q * j + i] = __float_as_uint(x[i]);
+                    }
                 }
                 if (sigmoid)
                     take(x, e0 + 32 * Q * j);
@@ -334,7 +335,7 @@ __device__ void route_token(const MoeRouteArgs& a, int64_t t, int warp, int lane
 constexpr int kRouteWarps = 4;  // of a block: on one token, or a token each
 
 template <typename TL, int W, int Q>
-__global__ void __launch_bounds__(32 * kRouteWarps) moe_route_kernel(MoeRouteArgs a)
+__global__ void __launch_bounds__(32 * kRouteWarps, 8) moe_route_kernel(MoeRouteArgs a)
 {
     pdl_launch_dependents();
     pdl_wait();
