@@ -350,7 +350,8 @@ MATMULS = [(1, 1, 1), (1, 4096, 7168), (2, 3, 16), (3, 130, 17), (4, 64, 64), (5
            (8, 1000, 2048), (9, 128, 128), (16, 256, 1024), (17, 100, 1025), (31, 257, 2049),
            (33, 1111, 1003), (64, 384, 4100), (65, 640, 512), (127, 200, 130), (128, 2048, 256),
            (129, 130, 3000), (200, 5000, 96), (300, 7168, 2048), (513, 777, 1500),
-           (1000, 4096, 700), (1537, 1300, 2304)]
+           (1000, 4096, 700), (1537, 1300, 2304), (160, 4096, 4500), (300, 2048, 6100),
+           (384, 9700, 1100), (1150, 9700, 700)]
 
 
 @pytest.mark.parametrize("T,N,K", MATMULS)

@@ -868,8 +868,8 @@ cudaError_t launch_type(const Int8Args& a, int sms, cudaStream_t s)
             return launch_cfg<CfgT32, T>(g, sms, s);
         return launch_cfg<CfgT128, T>(g, sms, s);
     }
-    // CTA pairs (N of their MMA is a multiple of 32): the token tile for which the
-    // rounds of units cost least, in clocks as measured: 64 codes take the MMAs' 2
+    // CTA pairs (N of their MMA is a multiple of 32): the token tile and the parts of
+    // K for which the rounds of units cost least, in clocks as measured: 64 codes take the MMAs' 2
     // nt clocks and the handshakes between the CTAs, at least 390 of the converters
     // (three groups, which leave registers for a tile of 128); a unit some 5000
     // more, and 8000 where its parts are joined
@@ -878,15 +878,16 @@ cudaError_t launch_type(const Int8Args& a, int sms, cudaStream_t s)
     int64_t best = INT64_MAX, units = 0;
     for (int nt = CfgP192::NTMAX; nt >= 64; nt -= 32) {
         const int64_t u = (a.T + nt - 1) / nt * g.n_tiles;
-        const int split = split_of(u, 2, a.K, sms);
         const int64_t item = nt <= CfgP128::NTMAX ? 390 : 2 * nt + 110;
-        const int64_t rounds = (u * split + pairs - 1) / pairs;
-        const int64_t cost = rounds * (items / split * item + (split > 1 ? 13000 : 5000));
-        if (cost < best) {
-            best = cost;
-            units = u;
-            g.nt = nt;
-            g.split = split;
+        for (int split = split_of(u, 2, a.K, sms); split >= 1; split /= 2) {
+            const int64_t rounds = split > 1 ? 1 : (u + pairs - 1) / pairs;
+            const int64_t cost = rounds * (items / split * item + (split > 1 ? 13000 : 5000));
+            if (cost < best) {
+                best = cost;
+                units = u;
+                g.nt = nt;
+                g.split = split;
+            }
         }
     }
     if (units > INT32_MAX)

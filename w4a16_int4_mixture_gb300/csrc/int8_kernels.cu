@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(256)
 //   1 token: dp4a 4.3, mma.sync 5.5;  8: dp4a 24.6, mma.sync on integers 6.3, on
 //   fp16 7.3;  16: on integers 10.3, on fp16 9 to 12 (its codes converted here)
 constexpr int kRowsM = 16;     // channels of a warp (the MMA's M)
-constexpr int kRowsWarps = 16;  // warps of a block: parts of K, or channel groups
+constexpr int kRowsWarps = 16;  // most warps of a block: parts of K, or channel groups
 constexpr int kRowsK = 64;     // codes of a step: two MMAs of K = 32
 constexpr int kRowsAhead = 2;  // steps whose loads are in flight
 
@@ -285,7 +285,8 @@ __global__ void __launch_bounds__(32 * kRowsWarps) int8_rows_kernel(Int8Args a, 
     constexpr int NX = NB == 0 ? 1 : NB;      // token rows of a lane
     __shared__ int part[kRowsWarps][kRowsM * NT];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = lane >> 2, c = lane & 3;
-    const int n0 = (blockIdx.x * (kRowsWarps / ks) + warp / ks) * kRowsM;
+    const int groups = static_cast<int>(blockDim.x >> 5) / ks;  // of channels, in this block
+    const int n0 = (blockIdx.x * groups + warp / ks) * kRowsM;
     const int8_t* wr[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -372,9 +373,9 @@ __global__ void __launch_bounds__(32 * kRowsWarps) int8_rows_kernel(Int8Args a, 
     }
     __syncthreads();
     // one output a thread: the sum of the parts
-    for (int o = threadIdx.x; o < (kRowsWarps / ks) * kRowsM * NT; o += 32 * kRowsWarps) {
+    for (int o = threadIdx.x; o < groups * kRowsM * NT; o += blockDim.x) {
         const int grp = o / (kRowsM * NT), at = o % (kRowsM * NT), t = at / kRowsM;
-        const int n = (blockIdx.x * (kRowsWarps / ks) + grp) * kRowsM + at % kRowsM;
+        const int n = (blockIdx.x * groups + grp) * kRowsM + at % kRowsM;
         if (n < a.N && t < a.T) {
             int sum = 0;
             for (int k = 0; k < ks; ++k)
@@ -396,13 +397,16 @@ cudaError_t launch_rows_type(const Int8Args& a, int sms, cudaStream_t s)
     const int64_t groups = (a.N + kRowsM - 1) / kRowsM;
     while (ks < kRowsWarps && groups * ks < 16 * static_cast<int64_t>(sms) && a.K > 4 * kRowsK * ks)
         ks *= 2;
-    const int per_block = kRowsWarps / ks;
-    const int grid = static_cast<int>((groups + per_block - 1) / per_block);
+    // smaller blocks where large ones would leave SMs without one
+    int warps = kRowsWarps;
+    while (warps > ks && (groups * ks + warps - 1) / warps < sms)
+        warps /= 2;
+    const int64_t grid = (groups * ks + warps - 1) / warps;
     if (a.T == 1)
-        return launch_pdl(int8_rows_kernel<T, 0>, grid, 32 * kRowsWarps, 0, s, a, ks);
+        return launch_pdl(int8_rows_kernel<T, 0>, static_cast<unsigned>(grid), 32 * warps, 0, s, a, ks);
     if (a.T <= 8)
-        return launch_pdl(int8_rows_kernel<T, 1>, grid, 32 * kRowsWarps, 0, s, a, ks);
-    return launch_pdl(int8_rows_kernel<T, 2>, grid, 32 * kRowsWarps, 0, s, a, ks);
+        return launch_pdl(int8_rows_kernel<T, 1>, static_cast<unsigned>(grid), 32 * warps, 0, s, a, ks);
+    return launch_pdl(int8_rows_kernel<T, 2>, static_cast<unsigned>(grid), 32 * warps, 0, s, a, ks);
 }
 
 template <typename T, bool SILU>
