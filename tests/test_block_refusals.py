@@ -111,3 +111,16 @@ def test_wrappers_refuse_host_tensors_and_wrong_types():
         chord.int8_matmul(torch.zeros(2, 16), torch.zeros(2), torch.zeros(3, 16), torch.zeros(3))
     with pytest.raises(TypeError):
         chord.int8_mlp(None, None, None, None, None)
+
+
+def test_quantize_and_rows_refuse_what_is_no_matrix_of_their_type():
+    import w4a16_int4_mixture_gb300 as chord
+
+    with pytest.raises(TypeError):
+        chord.int8_quantize(None)
+    with pytest.raises(TypeError, match="int8"):
+        chord.int8_rows(torch.zeros(2, 5))
+    with pytest.raises(ValueError, match="2 dims"):
+        chord.int8_rows(torch.zeros(5, dtype=torch.int8))
+    rows = chord.int8_rows(torch.arange(10, dtype=torch.int8).view(2, 5))
+    assert rows.stride() == (16, 1) and rows.tolist() == [[0, 1, 2, 3, 4], [5, 6, 7, 8, 9]]

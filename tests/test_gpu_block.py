@@ -573,3 +573,27 @@ def test_mixture_block(chord):
     assert torch.equal(y, chord.int8_mlp(x, w13, s13, w2, s2, residual=routed))
     packed = chord.prepack_weights(*wts)
     assert torch.equal(chord.moe_block(x, logits, s.k, packed, flags=2, **kw), routed)
+
+
+def test_threads_on_one_stream(chord):
+    """Two host threads whose calls' launches mix on one stream do not share a workspace."""
+    import threading
+
+    g = torch.Generator(device="cuda").manual_seed(8)
+    w13, s13 = chord.int8_quantize(torch.randn(256, 384, device=DEV, generator=g) / 20)
+    w2, s2 = chord.int8_quantize(torch.randn(384, 128, device=DEV, generator=g) / 11)
+    xs = [torch.randn(40, 384, device=DEV, generator=g) for _ in range(2)]
+    want = [chord.int8_mlp(x, w13, s13, w2, s2) for x in xs]
+    got = [[], []]
+
+    def calls(i):
+        for _ in range(200):
+            got[i].append(chord.int8_mlp(xs[i], w13, s13, w2, s2))
+
+    threads = [threading.Thread(target=calls, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i in range(2):
+        assert len(got[i]) == 200 and all(torch.equal(y, want[i]) for y in got[i])

@@ -14,6 +14,7 @@ contiguous):
 from __future__ import annotations
 
 import functools
+import threading
 from typing import Optional
 
 import torch
@@ -95,22 +96,26 @@ def _residual(t, dev, dtype, shape) -> int:
     return 0 if t is None else _rows(t, "residual", (dtype,), dev, shape)
 
 
-_spaces = {}
+_KEPT = 1 << 25  # bytes of the largest workspace that is kept
+_kept = threading.local()
 
 
 def _workspace(ws, dev, need: int, stream: int):
-    """The caller's workspace, or a buffer kept for each stream and grown on demand (an allocation
-    costs a call of one token a fifth of its host time).  Calls on one stream run in order, so
-    they share it; a captured graph, which may be replayed on any stream, gets its own."""
+    """The caller's workspace, or a buffer kept for each thread and stream and grown on demand (an
+    allocation costs a call of one token a fifth of its host time).  A thread's calls on one stream
+    run in order, so they share it; another thread's launches could come between those of a call.
+    A captured graph, which may be replayed on any stream, gets its own, and so does a large call,
+    whose host time does not count."""
     if ws is not None:
         ops._req(ws, "workspace", (torch.uint8,), dev, 1)
         return ws
-    if torch.cuda.is_current_stream_capturing():
+    if need > _KEPT or torch.cuda.is_current_stream_capturing():
         return torch.empty(need, dtype=torch.uint8, device=dev)
+    spaces = _kept.__dict__
     key = (dev.index, stream)
-    ws = _spaces.get(key)
+    ws = spaces.get(key)
     if ws is None or ws.numel() < need:
-        ws = _spaces[key] = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws = spaces[key] = torch.empty(need, dtype=torch.uint8, device=dev)
     return ws
 
 
@@ -188,6 +193,10 @@ def moe_route_backward(d_weights: torch.Tensor, logits: torch.Tensor, topk_ids: 
 
 def int8_rows(codes: torch.Tensor) -> torch.Tensor:
     """Codes int8 [N, K] copied to rows that start on 16-byte boundaries."""
+    if codes.dtype != torch.int8:
+        raise TypeError(f"codes: dtype {codes.dtype} is not torch.int8")
+    if codes.dim() != 2:
+        raise ValueError("codes must have 2 dims")
     N, K = codes.shape
     q = torch.empty((N, (K + 15) // 16 * 16), dtype=torch.int8, device=codes.device)[:, :K]
     q.copy_(codes)
@@ -214,7 +223,8 @@ def int8_quantize(x: torch.Tensor, out=None):
     """Rows of x [T, K] -> (codes int8 [T, K], scales float32 [T]): scale = max|x| / 127, codes =
     rint(x * (127 * (1 / max|x|))).  For tokens and for weights [N, K].  A row holding an inf or NaN
     gets the scale NaN.  The codes' rows start on 16-byte boundaries."""
-    return _quantize(x, x.shape[-1], _rows(x, "x", _TYPES), out, "chord_int8_quantize")
+    ld = _rows(x, "x", _TYPES)
+    return _quantize(x, x.shape[1], ld, out, "chord_int8_quantize")
 
 
 def int8_silu_mul_quantize(gate_up: torch.Tensor, out=None):

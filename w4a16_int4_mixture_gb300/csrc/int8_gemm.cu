@@ -869,10 +869,10 @@ cudaError_t launch_type(const Int8Args& a, int sms, cudaStream_t s)
         return launch_cfg<CfgT128, T>(g, sms, s);
     }
     // CTA pairs (N of their MMA is a multiple of 32): the token tile and the parts of
-    // K for which the rounds of units cost least, in clocks as measured: 64 codes take the MMAs' 2
-    // nt clocks and the handshakes between the CTAs, at least 390 of the converters
-    // (three groups, which leave registers for a tile of 128); a unit some 5000
-    // more, and 8000 where its parts are joined
+    // K for which the rounds of units cost least, in clocks as measured: 64 codes take
+    // the MMAs' 2 nt clocks and the handshakes between the CTAs, at least 390 of the
+    // converters (three groups, which leave registers for a tile of 128); a unit some
+    // 5000 more, and 8000 on top where its parts are joined
     g.n_tiles = (a.N + 2 * kTileM - 1) / (2 * kTileM);
     const int64_t items = (a.K + kHalfK - 1) / kHalfK, pairs = sms / 2;
     int64_t best = INT64_MAX, units = 0;
